@@ -36,7 +36,9 @@ EXPORTED = ("gnf4_last_error", "gnf4_version", "gnf4_quantize_nf4", "gnf4_quanti
             "gnf4_device_status", "gnf4_swiglu", "gnf4_combine_topk", "gnf4_dgrad_nf4",
             "gnf4_dgrad_mxfp4", "gnf4_routing_metadata", "gnf4_grouped_gemm_nf4_ex",
             "gnf4_grouped_gemm_mxfp4_ex", "gnf4_absmax_to_bf16", "gnf4_grouped_gemm_swiglu_nf4",
-            "gnf4_grouped_gemm_swiglu_mxfp4")
+            "gnf4_grouped_gemm_swiglu_mxfp4", "gnf4_quantize_act8", "gnf4_dequantize_act8",
+            "gnf4_swiglu_act8", "gnf4_swiglu_backward", "gnf4_lora_apply", "gnf4_lora_backward",
+            "gnf4_lora_grad_a")
 
 if not os.path.exists(LIB_PATH):
     raise ImportError(f"{LIB_PATH} is missing: build it with "
@@ -78,6 +80,22 @@ lib.gnf4_swiglu.restype = _i32
 lib.gnf4_swiglu.argtypes = [_p, _i64, _i64, _p, _p]
 lib.gnf4_combine_topk.restype = _i32
 lib.gnf4_combine_topk.argtypes = [_p, _i64, _i64, _p, _p, _i64, _i64, _p, _p]
+lib.gnf4_quantize_act8.restype = _i32
+lib.gnf4_quantize_act8.argtypes = [_p, _i64, _i64, _p, _p, _p]
+lib.gnf4_dequantize_act8.restype = _i32
+lib.gnf4_dequantize_act8.argtypes = [_p, _p, _i64, _i64, _p, _p]
+lib.gnf4_swiglu_act8.restype = _i32
+lib.gnf4_swiglu_act8.argtypes = [_p, _i64, _i64, _p, _p, _p, _p]
+lib.gnf4_swiglu_backward.restype = _i32
+lib.gnf4_swiglu_backward.argtypes = [_p, _p, _p, _p, _i64, _i64, _p, _p, _p]
+lib.gnf4_lora_apply.restype = _i32
+lib.gnf4_lora_apply.argtypes = [_p, _p, _i32, _p, _p, _p, _p, _p, _p, _p, _i64, _i64, _i64, _i64, _i64, _i64, _i64,
+                                _p, _p, _i32, _p]
+lib.gnf4_lora_backward.restype = _i32
+lib.gnf4_lora_backward.argtypes = [_p, _p, _p, _p, _p, _p, _p, _p, _p, _p, _p, _p, _i64, _i64, _i64, _i64, _i64, _i64,
+                                   _i64, _p, _p, _p, _p, _p, _i32, _i32, _p]
+lib.gnf4_lora_grad_a.restype = _i32
+lib.gnf4_lora_grad_a.argtypes = [_p, _p, _p, _p, _p, _p, _i64, _i64, _i64, _i64, _i64, _p, _i32, _i32, _p]
 lib.gnf4_device_status.restype = _i32
 lib.gnf4_device_status.argtypes = [_p]
 lib.gnf4_grouped_gemm_launches.restype = _i32

@@ -306,6 +306,254 @@ def combine_topk(y: torch.Tensor, T: int, k: int, row_of_slot: Optional[torch.Te
     return out
 
 
+def _shaped(t: Optional[torch.Tensor], shape, dtype: torch.dtype, name: str, like: torch.Tensor) -> torch.Tensor:
+    """``t`` checked against a type and shape, or a new tensor beside ``like`` if it is None."""
+    if t is None:
+        return torch.empty(shape, dtype=dtype, device=like.device)
+    _need(t, dtype, name)
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+    return t
+
+
+def _act8(act8, K: int, name: str):
+    """A checkpoint (codes int8 ``[rows, K]``, scales uint8 ``[rows, K/32]``), checked."""
+    codes, scales = act8
+    _need(codes, torch.int8, f"{name} codes")
+    _need(scales, torch.uint8, f"{name} scales")
+    if codes.dim() != 2 or codes.shape[1] != K or tuple(scales.shape) != (codes.shape[0], K // 32):
+        raise ValueError(f"{name} must be codes [rows, {K}] and scales [rows, {K // 32}], got "
+                         f"{list(codes.shape)} and {list(scales.shape)}")
+    return codes, scales
+
+
+def quantize_act8(x: torch.Tensor, codes: Optional[torch.Tensor] = None, scales: Optional[torch.Tensor] = None,
+                  stream=None):
+    """8-bit checkpoint of bf16 ``[..., K]`` rows: (codes int8 ``[..., K]``, scales uint8
+    ``[..., K//32]``), one e8m0 scale per 32 elements (include/gnf4.h)."""
+    _need(x, torch.bfloat16, "x")
+    K = x.shape[-1]
+    codes = _shaped(codes, x.shape, torch.int8, "codes", x)
+    scales = _shaped(scales, tuple(x.shape[:-1]) + (K // 32,), torch.uint8, "scales", x)
+    check(lib.gnf4_quantize_act8(_ptr(x), x.numel() // K if K else 0, K, _ptr(codes), _ptr(scales), _stream(stream)),
+          "gnf4_quantize_act8")
+    return codes, scales
+
+
+def dequantize_act8(codes: torch.Tensor, scales: torch.Tensor, out: Optional[torch.Tensor] = None,
+                    stream=None) -> torch.Tensor:
+    """The bf16 values an 8-bit checkpoint stands for (include/gnf4.h)."""
+    _need(codes, torch.int8, "codes")
+    K = codes.shape[-1]
+    _need(scales, torch.uint8, "scales")
+    if tuple(scales.shape) != tuple(codes.shape[:-1]) + (K // 32,):
+        raise ValueError(f"scales must be [..., {K // 32}] beside codes {list(codes.shape)}, got {list(scales.shape)}")
+    out = _shaped(out, codes.shape, torch.bfloat16, "out", codes)
+    check(lib.gnf4_dequantize_act8(_ptr(codes), _ptr(scales), codes.numel() // K if K else 0, K, _ptr(out),
+                                   _stream(stream)), "gnf4_dequantize_act8")
+    return out
+
+
+def swiglu_act8(gate_up: torch.Tensor, out: Optional[torch.Tensor] = None, codes: Optional[torch.Tensor] = None,
+                scales: Optional[torch.Tensor] = None, stream=None):
+    """``swiglu`` and the 8-bit checkpoint of its ``[R, 2I]`` input in one pass: (out ``[R, I]``,
+    codes ``[R, 2I]``, scales ``[R, 2I/32]``) (include/gnf4.h)."""
+    _need(gate_up, torch.bfloat16, "gate_up")
+    if gate_up.dim() != 2 or gate_up.shape[1] % 2:
+        raise ValueError(f"gate_up must be [R, 2I], got {tuple(gate_up.shape)}")
+    R, I = gate_up.shape[0], gate_up.shape[1] // 2
+    out = _shaped(out, (R, I), torch.bfloat16, "out", gate_up)
+    codes = _shaped(codes, (R, 2 * I), torch.int8, "codes", gate_up)
+    scales = _shaped(scales, (R, 2 * I // 32), torch.uint8, "scales", gate_up)
+    check(lib.gnf4_swiglu_act8(_ptr(gate_up), R, I, _ptr(out), _ptr(codes), _ptr(scales), _stream(stream)),
+          "gnf4_swiglu_act8")
+    return out, codes, scales
+
+
+def swiglu_backward(grad_out: torch.Tensor, gate_up: Optional[torch.Tensor] = None, act8=None,
+                    out: Optional[torch.Tensor] = None, rebuild: bool = False, act: Optional[torch.Tensor] = None,
+                    stream=None):
+    """Gradient of ``swiglu``'s input, bf16 ``[R, 2I]``, from ``grad_out`` ``[R, I]`` and either the
+    ``gate_up`` rows or their checkpoint ``act8 = (codes, scales)``. With ``rebuild`` (or ``act``
+    given) returns (gradient, the activations ``[R, I]`` once more), else the gradient alone
+    (include/gnf4.h)."""
+    _need(grad_out, torch.bfloat16, "grad_out")
+    if grad_out.dim() != 2:
+        raise ValueError("grad_out must be [R, I]")
+    R, I = grad_out.shape
+    if (gate_up is None) == (act8 is None):
+        raise ValueError("give either gate_up or act8")
+    codes = scales = None
+    if gate_up is not None:
+        gate_up = _shaped(gate_up, (R, 2 * I), torch.bfloat16, "gate_up", grad_out)
+    else:
+        codes, scales = _act8(act8, 2 * I, "act8")
+        if codes.shape[0] != R:
+            raise ValueError(f"act8 must hold {R} rows, got {codes.shape[0]}")
+    out = _shaped(out, (R, 2 * I), torch.bfloat16, "out", grad_out)
+    if rebuild or act is not None:
+        act = _shaped(act, (R, I), torch.bfloat16, "act", grad_out)
+    check(lib.gnf4_swiglu_backward(_ptr(grad_out), _ptr(gate_up), _ptr(codes), _ptr(scales), R, I, _ptr(out),
+                                   _ptr(act), _stream(stream)), "gnf4_swiglu_backward")
+    return out if act is None else (out, act)
+
+
+def _lora_common(A, B, adapter_offsets, row_token, row_weight, rows, scaling, R, dtype):
+    _need(A, dtype, "A")
+    _need(B, dtype, "B")
+    if A.dim() != 3 or B.dim() != 3 or A.shape[0] != B.shape[0] or A.shape[1] != B.shape[2]:
+        raise ValueError(f"A must be [L, r, K] and B [L, N, r], got {list(A.shape)} and {list(B.shape)}")
+    L, r, K = A.shape
+    _need(adapter_offsets, torch.int64, "adapter_offsets")
+    if adapter_offsets.numel() != L + 1:
+        raise ValueError(f"adapter_offsets must hold L + 1 = {L + 1} entries, got {adapter_offsets.numel()}")
+    arrays = (("row_token", row_token, torch.int32), ("row_weight", row_weight, torch.float32), rows)
+    for name, t, dt in arrays:
+        if t is not None:
+            _need(t, dt, name)
+            if R is None:
+                R = t.numel()
+            if t.numel() < R:
+                raise ValueError(f"{name} must hold R = {R} entries, got {t.numel()}")
+    if scaling is not None:
+        _need(scaling, torch.float32, "scaling")
+        if scaling.numel() != L:
+            raise ValueError(f"scaling must hold L = {L} entries, got {scaling.numel()}")
+    return L, r, K, B.shape[1], R
+
+
+def _lora_x(x, act8, K: int):
+    """The adapters' input as bf16 rows or as a checkpoint: (codes, scales, rows)."""
+    if (x is None) == (act8 is None):
+        raise ValueError("give either x or act8")
+    if x is None:
+        codes, scales = _act8(act8, K, "act8")
+        return codes, scales, codes.shape[0]
+    _need(x, torch.bfloat16, "x")
+    if x.dim() != 2 or x.shape[1] != K:
+        raise ValueError(f"x must be [T_in, K = {K}], got {list(x.shape)}")
+    return None, None, x.shape[0]
+
+
+def lora_apply(base: Optional[torch.Tensor], x: torch.Tensor, A: torch.Tensor, B: torch.Tensor,
+               adapter_offsets: torch.Tensor, row_token: Optional[torch.Tensor] = None,
+               row_weight: Optional[torch.Tensor] = None, row_dest: Optional[torch.Tensor] = None,
+               scaling: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None,
+               h: Optional[torch.Tensor] = None, R: Optional[int] = None, flags: int = 0, stream=None) -> torch.Tensor:
+    """Low-rank adapters on top of a projection's output, all adapters in one launch
+    (include/gnf4.h, gnf4_lora_apply): ``out[dest r] = base[dest r] + scaling[e] w(r) B[e] (A[e]
+    x[tok r])`` for the rows r of adapter e, sorted as ``adapter_offsets`` says. ``A`` ``[L, r, K]``,
+    ``B`` ``[L, N, r]``, all of ``x``'s type (bf16 or fp16). ``out`` defaults to ``base`` (in place).
+    ``h`` (fp32 ``[R, r]``) receives what ``lora_backward`` needs. ``R``: the rows' number or an
+    upper bound of it, taken from the row arrays when it is not given, else from ``x``."""
+    if x.dtype not in (torch.bfloat16, torch.float16):
+        raise TypeError(f"x must be torch.bfloat16 or torch.float16, got {x.dtype}")
+    _need(x, x.dtype, "x")
+    L, r, K, N, R = _lora_common(A, B, adapter_offsets, row_token, row_weight, ("row_dest", row_dest, torch.int32),
+                                 scaling, R, x.dtype)
+    if x.dim() != 2 or x.shape[1] != K:
+        raise ValueError(f"x must be [T_in, K = {K}], got {list(x.shape)}")
+    if R is None:
+        R = x.shape[0]
+    if base is None and out is None:
+        raise ValueError("give base, or out (then the adapters' product alone is written there)")
+    if out is None:
+        out = base
+    for name, t in (("base", base), ("out", out)):
+        if t is not None:
+            _need(t, x.dtype, name)
+            if t.dim() != 2 or t.shape != out.shape or t.shape[1] != N:
+                raise ValueError(f"{name} must be [T_out, N = {N}] (base and out alike), got {list(t.shape)}")
+    if h is not None:
+        h = _shaped(h, (R, r), torch.float32, "h", x)
+    xdt = _lib.GNF4_DTYPE_F16 if x.dtype == torch.float16 else _lib.GNF4_DTYPE_BF16
+    check(lib.gnf4_lora_apply(_ptr(base), _ptr(x), xdt, _ptr(A), _ptr(B), _ptr(adapter_offsets), _ptr(row_token),
+                              _ptr(row_weight), _ptr(row_dest), _ptr(scaling), L, r, N, K, R, x.shape[0],
+                              out.shape[0], _ptr(out), _ptr(h), flags, _stream(stream)), "gnf4_lora_apply")
+    return out
+
+
+def lora_backward(grad_out: torch.Tensor, h: torch.Tensor, A: torch.Tensor, B: torch.Tensor,
+                  adapter_offsets: torch.Tensor, x: Optional[torch.Tensor] = None, act8=None,
+                  row_token: Optional[torch.Tensor] = None, row_weight: Optional[torch.Tensor] = None,
+                  row_src: Optional[torch.Tensor] = None, scaling: Optional[torch.Tensor] = None,
+                  dx_base: Optional[torch.Tensor] = None, dx: Optional[torch.Tensor] = None, want_dx: bool = True,
+                  grad_dtype: torch.dtype = torch.bfloat16, dA: Optional[torch.Tensor] = None,
+                  dB: Optional[torch.Tensor] = None, grad_h: Optional[torch.Tensor] = None, R: Optional[int] = None,
+                  flags: int = 0, stream=None):
+    """Gradients of ``lora_apply`` (bf16; include/gnf4.h, gnf4_lora_backward): (dx bf16 ``[R, K]`` in
+    routed order on top of ``dx_base``, or None without ``want_dx``; dA ``[L, r, K]``; dB ``[L, N, r]``),
+    the last two in ``grad_dtype`` (bf16 or fp32). ``x`` is the forward's input or ``act8 = (codes,
+    scales)`` its checkpoint; with neither dA is None, and ``lora_grad_a`` gives it from ``grad_h``; ``h`` what the forward wrote; ``row_src`` its ``row_dest``. ``grad_h``
+    (fp32 ``[R, r]``) is the call's own buffer; it has to be given together with ``stream``."""
+    _need(grad_out, torch.bfloat16, "grad_out")
+    L, r, K, N, R = _lora_common(A, B, adapter_offsets, row_token, row_weight, ("row_src", row_src, torch.int32),
+                                 scaling, R, torch.bfloat16)
+    if grad_dtype not in (torch.bfloat16, torch.float32):
+        raise TypeError(f"grad_dtype must be torch.bfloat16 or torch.float32, got {grad_dtype}")
+    if grad_out.dim() != 2 or grad_out.shape[1] != N:
+        raise ValueError(f"grad_out must be [T_g, N = {N}], got {list(grad_out.shape)}")
+    if R is None:
+        R = h.shape[0]
+    if x is None and act8 is None:
+        codes = scales = None
+        T_in = R if row_token is None else 2 ** 31 - 1     # no row of x is read
+        if grad_h is None:
+            raise ValueError("without x and act8 there is no dA: pass grad_h, which lora_grad_a takes")
+        if dA is not None:
+            raise ValueError("dA needs x or act8")
+    else:
+        codes, scales, T_in = _lora_x(x, act8, K)
+    _shaped(h, (R, r), torch.float32, "h", grad_out)
+    if stream is not None and grad_h is None:
+        raise ValueError("pass grad_h with a stream of its own (a buffer made here would be reused too early)")
+    if dx_base is not None:
+        want_dx = True
+        _shaped(dx_base, (R, K), torch.bfloat16, "dx_base", grad_out)
+    if want_dx or dx is not None:
+        dx = _shaped(dx, (R, K), torch.bfloat16, "dx", grad_out)
+    if x is not None or act8 is not None:
+        dA = _shaped(dA, (L, r, K), grad_dtype, "dA", grad_out)
+    dB = _shaped(dB, (L, N, r), grad_dtype, "dB", grad_out)
+    grad_h = _shaped(grad_h, (R, r), torch.float32, "grad_h", grad_out)
+    gdt = _lib.GNF4_DTYPE_F32 if grad_dtype == torch.float32 else _lib.GNF4_DTYPE_BF16
+    check(lib.gnf4_lora_backward(_ptr(grad_out), _ptr(x), _ptr(codes), _ptr(scales), _ptr(h), _ptr(A), _ptr(B),
+                                 _ptr(adapter_offsets), _ptr(row_token), _ptr(row_weight), _ptr(row_src),
+                                 _ptr(scaling), L, r, N, K, R, T_in, grad_out.shape[0], _ptr(dx_base), _ptr(dx),
+                                 _ptr(grad_h), _ptr(dA), _ptr(dB), gdt, flags, _stream(stream)),
+          "gnf4_lora_backward")
+    return dx, dA, dB
+
+
+def lora_grad_a(grad_h: torch.Tensor, adapter_offsets: torch.Tensor, x: Optional[torch.Tensor] = None, act8=None,
+                row_token: Optional[torch.Tensor] = None, grad_dtype: torch.dtype = torch.bfloat16,
+                dA: Optional[torch.Tensor] = None, flags: int = 0, stream=None) -> torch.Tensor:
+    """dA ``[L, r, K]`` alone, from the ``grad_h`` ``[R, r]`` of a ``lora_backward`` without x
+    (include/gnf4.h, gnf4_lora_grad_a)."""
+    _need(grad_h, torch.float32, "grad_h")
+    _need(adapter_offsets, torch.int64, "adapter_offsets")
+    if grad_dtype not in (torch.bfloat16, torch.float32):
+        raise TypeError(f"grad_dtype must be torch.bfloat16 or torch.float32, got {grad_dtype}")
+    if grad_h.dim() != 2:
+        raise ValueError(f"grad_h must be [R, r], got {list(grad_h.shape)}")
+    (R, r), L = grad_h.shape, adapter_offsets.numel() - 1
+    rows = x if act8 is None else act8[0]
+    if rows is None or rows.dim() != 2:
+        raise ValueError("give either x or act8, with rows [T_in, K]")
+    K = rows.shape[1]
+    codes, scales, T_in = _lora_x(x, act8, K)
+    if row_token is not None:
+        _need(row_token, torch.int32, "row_token")
+        if row_token.numel() < R:
+            raise ValueError(f"row_token must hold R = {R} entries, got {row_token.numel()}")
+    dA = _shaped(dA, (L, r, K), grad_dtype, "dA", grad_h)
+    gdt = _lib.GNF4_DTYPE_F32 if grad_dtype == torch.float32 else _lib.GNF4_DTYPE_BF16
+    check(lib.gnf4_lora_grad_a(_ptr(grad_h), _ptr(x), _ptr(codes), _ptr(scales), _ptr(adapter_offsets),
+                               _ptr(row_token), L, r, K, R, T_in, _ptr(dA), gdt, flags, _stream(stream)),
+          "gnf4_lora_grad_a")
+    return dA
+
+
 def device_status(stream=None) -> None:
     """Synchronise the stream; raise if a kernel gave up waiting on a barrier."""
     check(lib.gnf4_device_status(_stream(stream)), "gnf4_device_status")

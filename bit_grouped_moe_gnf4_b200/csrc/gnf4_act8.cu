@@ -1,0 +1,308 @@
+// 8-bit activation checkpoints and the SwiGLU's backward pass.
+//
+// Format (OCP MXINT8: int8 elements, one e8m0 scale per 32 along the row): for a block of
+// 32 bf16 values, s is the exponent field of the largest magnitude (floor(log2) + 127, 0
+// for zeros and subnormals), a code c is the value in steps of 2^(s-133), rounded to
+// nearest even and clamped to +-127, and it stands for c * 2^(s-133). bf16 has 8
+// significant bits, so the largest value of a block is at most 127.5 steps and no value is
+// off by more than half a step; every c * 2^(s-133) is itself a bf16 number. A block with
+// an infinity or a NaN has s = 255 and codes 0, and all of it reads back as NaN.
+//
+// All four kernels stream 16-byte vectors of 8 bf16 (8 codes are 8 bytes); four
+// neighbouring lanes hold one block of 32, so a block's scale is two shuffles. They are
+// bound by HBM: the arithmetic is about 6 instructions an element for the codes and 15 for
+// the SwiGLU's gradients.
+#include <cstdint>
+#include <cuda_runtime.h>
+
+#include "gnf4_act8.cuh"
+#include "gnf4_kernels.h"
+
+namespace gnf4 {
+
+namespace {
+
+constexpr int kActThreads = 256;
+constexpr int kActCtasPerSm = 8;
+constexpr int kActVecs = 4;            // 16-byte vectors per thread and pass (loads issued together)
+constexpr int kSwigluActVecs = 2;      // the SwiGLU kernels hold three or four arrays per vector
+
+__device__ __forceinline__ float lo_f(uint32_t w) { return __uint_as_float(w << 16); }
+__device__ __forceinline__ float hi_f(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
+
+__device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
+    uint32_t d;
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
+    return d;
+}
+
+// the block's scale: the largest exponent field of the 32 values held by four lanes
+__device__ __forceinline__ uint32_t block_scale(const uint4& v) {
+    uint32_t m = __vmaxu2(__vmaxu2(v.x & 0x7F807F80u, v.y & 0x7F807F80u),
+                          __vmaxu2(v.z & 0x7F807F80u, v.w & 0x7F807F80u));
+    m = max(m & 0xFFFFu, m >> 16);
+    m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
+    m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
+    return m >> 7;
+}
+
+// a value times 2^(133-s), rounded to nearest even and clamped, in the low byte: adding
+// 1.5 * 2^23 leaves the rounded integer in the low mantissa bits (two's complement)
+__device__ __forceinline__ uint32_t code_of(float scaled) {
+    return __float_as_uint(fminf(fmaxf(scaled, -127.0f), 127.0f) + 12582912.0f);
+}
+
+__device__ __forceinline__ uint2 encode8(const uint4& v, uint32_t s) {
+    if (s == 255u) return make_uint2(0u, 0u);
+    // 2^(133-s) is an fp32 number for s >= 6; below that in two exact steps
+    const float up = __uint_as_float((260u - max(s, 6u)) << 23);
+    const float more = __uint_as_float((127u + max(s, 6u) - s) << 23);
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+    uint32_t c[8];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        c[2 * i] = code_of(lo_f(w[i]) * more * up);
+        c[2 * i + 1] = code_of(hi_f(w[i]) * more * up);
+    }
+    uint2 o;
+    o.x = prmt(prmt(c[0], c[1], 0x0040u), prmt(c[2], c[3], 0x0040u), 0x5410u);
+    o.y = prmt(prmt(c[4], c[5], 0x0040u), prmt(c[6], c[7], 0x0040u), 0x5410u);
+    return o;
+}
+
+__device__ __forceinline__ uint4 decode8(const uint2& q, uint32_t s) {
+    float f[8];
+    act8_values(q, act8_step(s), f);
+    return make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]),
+                      pack_bf16x2(f[6], f[7]));
+}
+
+// total: 16-byte vectors; a multiple of 4, so the four lanes of a block are all in range or all out
+__global__ void __launch_bounds__(kActThreads) quantize_act8_kernel(const uint4* __restrict__ x, uint2* __restrict__ codes,
+                                                                    uint8_t* __restrict__ scales, int64_t total) {
+    const int64_t stride = (int64_t)gridDim.x * (kActThreads * kActVecs);
+    for (int64_t b = (int64_t)blockIdx.x * (kActThreads * kActVecs); b < total; b += stride) {
+        const int64_t base = b + threadIdx.x;
+        uint4 v[kActVecs];
+#pragma unroll
+        for (int j = 0; j < kActVecs; ++j) {
+            const int64_t i = base + j * kActThreads;
+            v[j] = i < total ? __ldg(x + i) : make_uint4(0u, 0u, 0u, 0u);
+        }
+#pragma unroll
+        for (int j = 0; j < kActVecs; ++j) {
+            const int64_t i = base + j * kActThreads;
+            const uint32_t s = block_scale(v[j]);
+            if (i < total) {
+                codes[i] = encode8(v[j], s);
+                if ((i & 3) == 0) scales[i >> 2] = (uint8_t)s;
+            }
+        }
+    }
+}
+
+__global__ void __launch_bounds__(kActThreads) dequantize_act8_kernel(const uint2* __restrict__ codes,
+                                                                      const uint8_t* __restrict__ scales,
+                                                                      uint4* __restrict__ out, int64_t total) {
+    const int64_t stride = (int64_t)gridDim.x * (kActThreads * kActVecs);
+    for (int64_t base = (int64_t)blockIdx.x * (kActThreads * kActVecs) + threadIdx.x; base < total; base += stride) {
+        uint2 q[kActVecs];
+        uint32_t s[kActVecs];
+#pragma unroll
+        for (int j = 0; j < kActVecs; ++j) {
+            const int64_t i = base + j * kActThreads;
+            if (i < total) {
+                q[j] = __ldg(codes + i);
+                s[j] = __ldg(scales + (i >> 2));
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < kActVecs; ++j) {
+            const int64_t i = base + j * kActThreads;
+            if (i < total) out[i] = decode8(q[j], s[j]);
+        }
+    }
+}
+
+__device__ __forceinline__ uint32_t silu_word(uint32_t g, uint32_t u) {
+    return pack_bf16x2(silu_mul(lo_f(g), lo_f(u)), silu_mul(hi_f(g), hi_f(u)));
+}
+
+// out = silu(gate) * up with the same instructions as gnf4_swiglu, and the checkpoint of
+// both halves. I8 = I / 8 vectors a row and half (a multiple of 4: blocks never straddle).
+template <typename IDX>
+__global__ void __launch_bounds__(kActThreads) swiglu_act8_kernel(const uint4* __restrict__ h, uint4* __restrict__ out,
+                                                                  uint2* __restrict__ codes,
+                                                                  uint8_t* __restrict__ scales, IDX I8, IDX total) {
+    const IDX stride = (IDX)gridDim.x * (kActThreads * kSwigluActVecs);
+    for (IDX b = (IDX)blockIdx.x * (kActThreads * kSwigluActVecs); b < total; b += stride) {
+        uint4 g[kSwigluActVecs], u[kSwigluActVecs];
+        int64_t at[kSwigluActVecs];              // vector index of the gate in the [R, 2I] rows
+#pragma unroll
+        for (int j = 0; j < kSwigluActVecs; ++j) {
+            const IDX i = b + threadIdx.x + (IDX)j * kActThreads;
+            g[j] = u[j] = make_uint4(0u, 0u, 0u, 0u);
+            at[j] = 0;
+            if (i < total) {
+                const IDX r = i / I8;
+                at[j] = (int64_t)i + (int64_t)r * I8;      // r * 2 I8 + (i - r I8)
+                g[j] = __ldg(h + at[j]);
+                u[j] = __ldg(h + at[j] + I8);
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < kSwigluActVecs; ++j) {
+            const IDX i = b + threadIdx.x + (IDX)j * kActThreads;
+            const uint32_t sg = block_scale(g[j]), su = block_scale(u[j]);
+            if (i < total) {
+                out[i] = make_uint4(silu_word(g[j].x, u[j].x), silu_word(g[j].y, u[j].y),
+                                    silu_word(g[j].z, u[j].z), silu_word(g[j].w, u[j].w));
+                codes[at[j]] = encode8(g[j], sg);
+                codes[at[j] + I8] = encode8(u[j], su);
+                if ((i & 3) == 0) {
+                    scales[at[j] >> 2] = (uint8_t)sg;
+                    scales[(at[j] + I8) >> 2] = (uint8_t)su;
+                }
+            }
+        }
+    }
+}
+
+// With e = exp(-|g|) and v = 1 / (1 + e): sigmoid(g) is v or e v by g's sign and 1 - sigmoid(g)
+// the other one, so neither is a difference of near numbers.
+//   d_gate = d * (u * sig (1 + g (1 - sig))),  d_up = d * (g sig)
+__device__ __forceinline__ void swiglu_grad(float g, float u, float d, float& dg, float& du) {
+    const float e = exp_via_ex2(-fabsf(g));
+    const float v = __fdividef(1.0f, 1.0f + e), ev = e * v;
+    const float sig = g >= 0.0f ? v : ev, rest = g >= 0.0f ? ev : v;
+    dg = d * (u * (sig * fmaf(g, rest, 1.0f)));
+    du = d * (g * sig);
+}
+
+__device__ __forceinline__ void swiglu_grad_word(uint32_t g, uint32_t u, uint32_t d, uint32_t& dg, uint32_t& du) {
+    float a0, a1, b0, b1;
+    swiglu_grad(lo_f(g), lo_f(u), lo_f(d), a0, b0);
+    swiglu_grad(hi_f(g), hi_f(u), hi_f(d), a1, b1);
+    dg = pack_bf16x2(a0, a1);
+    du = pack_bf16x2(b0, b1);
+}
+
+// Q8: gate_up comes from its checkpoint. again (may be null): silu(gate) * up once more.
+template <typename IDX, bool Q8>
+__global__ void __launch_bounds__(kActThreads) swiglu_backward_kernel(const uint4* __restrict__ d,
+                                                                      const uint4* __restrict__ h,
+                                                                      const uint2* __restrict__ codes,
+                                                                      const uint8_t* __restrict__ scales,
+                                                                      uint4* __restrict__ dh, uint4* __restrict__ again,
+                                                                      IDX I8, IDX total) {
+    const IDX stride = (IDX)gridDim.x * (kActThreads * kSwigluActVecs);
+    for (IDX base = (IDX)blockIdx.x * (kActThreads * kSwigluActVecs) + threadIdx.x; base < total; base += stride) {
+        uint4 g[kSwigluActVecs], u[kSwigluActVecs], dv[kSwigluActVecs];
+        uint2 qg[kSwigluActVecs], qu[kSwigluActVecs];
+        uint32_t sg[kSwigluActVecs], su[kSwigluActVecs];
+        int64_t at[kSwigluActVecs];
+#pragma unroll
+        for (int j = 0; j < kSwigluActVecs; ++j) {
+            const IDX i = base + (IDX)j * kActThreads;
+            if (i < total) {
+                const IDX r = i / I8;
+                at[j] = (int64_t)i + (int64_t)r * I8;
+                dv[j] = __ldg(d + i);
+                if (Q8) {
+                    qg[j] = __ldg(codes + at[j]);
+                    qu[j] = __ldg(codes + at[j] + I8);
+                    sg[j] = __ldg(scales + (at[j] >> 2));
+                    su[j] = __ldg(scales + ((at[j] + I8) >> 2));
+                } else {
+                    g[j] = __ldg(h + at[j]);
+                    u[j] = __ldg(h + at[j] + I8);
+                }
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < kSwigluActVecs; ++j) {
+            const IDX i = base + (IDX)j * kActThreads;
+            if (i < total) {
+                if (Q8) {
+                    g[j] = decode8(qg[j], sg[j]);
+                    u[j] = decode8(qu[j], su[j]);
+                }
+                uint4 dg, du;
+                swiglu_grad_word(g[j].x, u[j].x, dv[j].x, dg.x, du.x);
+                swiglu_grad_word(g[j].y, u[j].y, dv[j].y, dg.y, du.y);
+                swiglu_grad_word(g[j].z, u[j].z, dv[j].z, dg.z, du.z);
+                swiglu_grad_word(g[j].w, u[j].w, dv[j].w, dg.w, du.w);
+                dh[at[j]] = dg;
+                dh[at[j] + I8] = du;
+                if (again)
+                    again[i] = make_uint4(silu_word(g[j].x, u[j].x), silu_word(g[j].y, u[j].y),
+                                          silu_word(g[j].z, u[j].z), silu_word(g[j].w, u[j].w));
+            }
+        }
+    }
+}
+
+int act_grid(int64_t total, int per_thread) {
+    const int64_t per_cta = (int64_t)kActThreads * per_thread;
+    const int64_t want = (total + per_cta - 1) / per_cta;
+    const int64_t cap = (int64_t)device_sm_count() * kActCtasPerSm;
+    return (int)(want < cap ? want : cap);
+}
+
+// whether every index a 32-bit walk over `total` vectors forms fits in 32 bits
+bool fits_u32(int64_t total, int grid, int per_thread) {
+    return total <= (int64_t)UINT32_MAX - 2 * (int64_t)grid * kActThreads * per_thread;
+}
+
+}  // namespace
+
+cudaError_t launch_quantize_act8(const void* x, int64_t n, int8_t* codes, uint8_t* scales, cudaStream_t s) {
+    const int64_t total = n / 8;
+    quantize_act8_kernel<<<act_grid(total, kActVecs), kActThreads, 0, s>>>(
+        reinterpret_cast<const uint4*>(x), reinterpret_cast<uint2*>(codes), scales, total);
+    return cudaGetLastError();
+}
+
+cudaError_t launch_dequantize_act8(const int8_t* codes, const uint8_t* scales, int64_t n, void* out, cudaStream_t s) {
+    const int64_t total = n / 8;
+    dequantize_act8_kernel<<<act_grid(total, kActVecs), kActThreads, 0, s>>>(
+        reinterpret_cast<const uint2*>(codes), scales, reinterpret_cast<uint4*>(out), total);
+    return cudaGetLastError();
+}
+
+cudaError_t launch_swiglu_act8(const void* gate_up, int64_t R, int64_t I, void* out, int8_t* codes, uint8_t* scales,
+                               cudaStream_t s) {
+    const int64_t I8 = I / 8, total = R * I8;
+    const int grid = act_grid(total, kSwigluActVecs);
+    const uint4* h = reinterpret_cast<const uint4*>(gate_up);
+    uint4* o = reinterpret_cast<uint4*>(out);
+    uint2* q = reinterpret_cast<uint2*>(codes);
+    if (fits_u32(total, grid, kSwigluActVecs))
+        swiglu_act8_kernel<uint32_t><<<grid, kActThreads, 0, s>>>(h, o, q, scales, (uint32_t)I8, (uint32_t)total);
+    else
+        swiglu_act8_kernel<int64_t><<<grid, kActThreads, 0, s>>>(h, o, q, scales, I8, total);
+    return cudaGetLastError();
+}
+
+cudaError_t launch_swiglu_backward(const void* d_out, const void* gate_up, const int8_t* codes, const uint8_t* scales,
+                                   int64_t R, int64_t I, void* d_gate_up, void* again, cudaStream_t s) {
+    const int64_t I8 = I / 8, total = R * I8;
+    const int grid = act_grid(total, kSwigluActVecs);
+    const uint4* d = reinterpret_cast<const uint4*>(d_out);
+    const uint4* h = reinterpret_cast<const uint4*>(gate_up);
+    const uint2* q = reinterpret_cast<const uint2*>(codes);
+    uint4* dh = reinterpret_cast<uint4*>(d_gate_up);
+    uint4* a = reinterpret_cast<uint4*>(again);
+    const bool small = fits_u32(total, grid, kSwigluActVecs);
+    if (gate_up && small)
+        swiglu_backward_kernel<uint32_t, false><<<grid, kActThreads, 0, s>>>(d, h, q, scales, dh, a, (uint32_t)I8, (uint32_t)total);
+    else if (gate_up)
+        swiglu_backward_kernel<int64_t, false><<<grid, kActThreads, 0, s>>>(d, h, q, scales, dh, a, I8, total);
+    else if (small)
+        swiglu_backward_kernel<uint32_t, true><<<grid, kActThreads, 0, s>>>(d, h, q, scales, dh, a, (uint32_t)I8, (uint32_t)total);
+    else
+        swiglu_backward_kernel<int64_t, true><<<grid, kActThreads, 0, s>>>(d, h, q, scales, dh, a, I8, total);
+    return cudaGetLastError();
+}
+
+}  // namespace gnf4

@@ -5,6 +5,7 @@
 #include <cstdarg>
 #include <cstdio>
 #include <cstring>
+#include <initializer_list>
 #include <cuda_runtime.h>
 
 #include "../../include/gnf4.h"
@@ -371,6 +372,119 @@ static gnf4_status dgrad(int fmt, const void* grad_out, const uint8_t* W, const 
     return e == cudaSuccess ? GNF4_OK : cuda_fail(e, "dgrad launch");
 }
 
+static bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+static bool aligned8(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 7u) == 0; }
+
+// every buffer that is given (the last step of a check: alignment is refused before)
+static gnf4_status check_device(std::initializer_list<const void*> ptrs) {
+    for (const void* q : ptrs)
+        if (q && !is_device_ptr(q))
+            return fail(GNF4_ERR_INVALID_ARG, "every buffer must be device memory of the current device");
+    return GNF4_OK;
+}
+
+static gnf4_status check_act8_args(const void* x16, const void* codes, const void* scales) {
+    if (!x16 || !codes || !scales) return fail(GNF4_ERR_INVALID_ARG, "null pointer argument");
+    if (!aligned16(x16) || !aligned8(codes))
+        return fail(GNF4_ERR_MISALIGNED, "bf16 rows must be 16-byte and codes 8-byte aligned");
+    return check_device({x16, codes, scales});
+}
+
+// sizes of an [rows, K] checkpoint
+static gnf4_status check_act8_sizes(int64_t rows, int64_t K) {
+    if (rows < 0 || K < 1) return fail(GNF4_ERR_INVALID_ARG, "sizes must be rows >= 0 and K >= 1");
+    if (K % 32) return fail(GNF4_ERR_UNSUPPORTED_SHAPE, "K must be a multiple of 32");
+    if (rows > INT64_MAX / 2 / K) return fail(GNF4_ERR_UNSUPPORTED_SHAPE, "rows * K must fit in int64");
+    return GNF4_OK;
+}
+
+static gnf4_status check_swiglu_sizes(int64_t R, int64_t I, int64_t imul) {
+    if (R < 0 || I < 1) return fail(GNF4_ERR_INVALID_ARG, "sizes must be R >= 0 and I >= 1");
+    if (I % imul) return fail(GNF4_ERR_UNSUPPORTED_SHAPE, "I must be a multiple of %lld", (long long)imul);
+    if (R > INT64_MAX / 4 / I) return fail(GNF4_ERR_UNSUPPORTED_SHAPE, "R * 2I must fit in int64");
+    return GNF4_OK;
+}
+
+// what both adapter calls have in common: sizes, then (rows or not) the buffers
+struct LoraCommon {
+    const void *A, *B;
+    const int64_t* offsets;
+    const int32_t *row_a, *row_b;
+    const float *weight, *scaling;
+    int64_t L, r, N, K, R, n_a, n_b;
+    int flags;
+};
+
+static gnf4_status check_lora_sizes(const LoraCommon& c) {
+    if (c.L < 1 || c.r < 1 || c.N < 1 || c.K < 1 || c.R < 0 || c.n_a < 0 || c.n_b < 0)
+        return fail(GNF4_ERR_INVALID_ARG, "sizes must be L, r, N, K >= 1 and rows >= 0");
+    if (c.flags & ~GNF4_CHECK) return fail(GNF4_ERR_INVALID_ARG, "only GNF4_CHECK is accepted (flags 0x%x)", c.flags);
+    if (c.r % 8 || c.r > 128) return fail(GNF4_ERR_UNSUPPORTED_SHAPE, "the rank must be a multiple of 8 up to 128");
+    if (c.K % 8 || c.N % 8) return fail(GNF4_ERR_UNSUPPORTED_SHAPE, "K and N must be multiples of 8");
+    if (c.L > 2048) return fail(GNF4_ERR_UNSUPPORTED_SHAPE, "at most 2048 adapters");
+    if (c.K > (1 << 24) || c.N > (1 << 24) || c.R > INT_MAX || c.n_a > INT_MAX || c.n_b > INT_MAX)
+        return fail(GNF4_ERR_UNSUPPORTED_SHAPE, "K and N must be at most 2^24, row counts must fit in int32");
+    if (!c.row_a && c.n_a < c.R) return fail(GNF4_ERR_INVALID_ARG, "row_token is NULL but T_in < R");
+    if (!c.row_b && c.n_b < c.R) return fail(GNF4_ERR_INVALID_ARG, "the destination rows are NULL but there are fewer than R");
+    return GNF4_OK;
+}
+
+static gnf4_status check_lora_buffers(const LoraCommon& c) {
+    if (!c.A || !c.B || !c.offsets) return fail(GNF4_ERR_INVALID_ARG, "null pointer argument");
+    if (!aligned16(c.A) || !aligned16(c.B)) return fail(GNF4_ERR_MISALIGNED, "A and B must be 16-byte aligned");
+    if (!aligned8(c.offsets) || !aligned4(c.row_a) || !aligned4(c.row_b) || !aligned4(c.weight) || !aligned4(c.scaling))
+        return fail(GNF4_ERR_MISALIGNED, "adapter_offsets must be 8-byte, row arrays and scaling 4-byte aligned");
+    return GNF4_OK;
+}
+
+static gnf4_status check_lora_device(const LoraCommon& c) {
+    return check_device({c.A, c.B, c.offsets, c.row_a, c.row_b, c.weight, c.scaling});
+}
+
+// the forward's input as rows or as a checkpoint; `none`: neither (no gradient of A is asked for)
+static gnf4_status check_lora_x(const void* x, const void* codes, const void* scales, bool none) {
+    if (none && (x || codes || scales)) return fail(GNF4_ERR_INVALID_ARG, "x is given but dA is NULL");
+    if (!none && (x ? (codes || scales) : !(codes && scales)))
+        return fail(GNF4_ERR_INVALID_ARG, "give either x or its checkpoint (x_codes and x_scales)");
+    return GNF4_OK;
+}
+
+static LoraGradSide grad_a_side(const float* grad_h, const void* x, const int8_t* codes, const uint8_t* scales,
+                                const int32_t* row_token, int64_t T_in, int64_t K, void* dA) {
+    LoraGradSide d;
+    d.left = grad_h;
+    d.right = reinterpret_cast<const uint16_t*>(x);
+    d.codes = codes;
+    d.scales = scales;
+    d.row = row_token;
+    d.out = dA;
+    d.n = T_in;
+    d.C = (int)K;
+    d.factor = 0;
+    d.transposed = 0;
+    return d;
+}
+
+// GNF4_CHECK of the adapter calls (one kernel and a stream sync)
+static gnf4_status check_lora_rows(const LoraCommon& c, cudaStream_t s) {
+    const int slot = (int)(g_check_next.fetch_add(1u, std::memory_order_relaxed) % kCheckSlots);
+    const size_t off = sizeof(unsigned) * (size_t)slot;
+    unsigned st = 0;
+    void* words = nullptr;
+    cudaError_t e = cudaGetSymbolAddress(&words, g_check_status);
+    if (e == cudaSuccess) e = cudaMemcpyToSymbolAsync(g_check_status, &st, sizeof(st), off, cudaMemcpyHostToDevice, s);
+    if (e == cudaSuccess)
+        e = launch_check_lora(c.offsets, (int)c.L, c.R, c.row_a, c.n_a, c.row_b, c.n_b, c.weight,
+                              reinterpret_cast<unsigned*>(words) + slot, s);
+    if (e == cudaSuccess) e = cudaMemcpyFromSymbolAsync(&st, g_check_status, sizeof(st), off, cudaMemcpyDeviceToHost, s);
+    if (e == cudaSuccess) e = cudaStreamSynchronize(s);
+    if (e != cudaSuccess) return cuda_fail(e, "adapter routing check");
+    if (st) return fail(GNF4_ERR_DEVICE_STATUS,
+                        "bad adapter rows (status 0x%x: 1 offsets decrease or pass R, 2 offsets[0] != 0, "
+                        "4 row_token out of range, 8 destination row out of range, 16 non-finite row_weight)", st);
+    return GNF4_OK;
+}
+
 }  // namespace gnf4
 
 using namespace gnf4;
@@ -553,6 +667,191 @@ gnf4_status gnf4_routing_metadata(const int32_t* topk_ids, const float* topk_wei
     cudaError_t e = launch_routing(topk_ids, topk_weights, T, k, (int)E, expert_offsets, row_token, row_weight,
                                    row_dest, reinterpret_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? GNF4_OK : cuda_fail(e, "routing launch");
+}
+
+gnf4_status gnf4_quantize_act8(const void* x, int64_t rows, int64_t K, int8_t* codes, uint8_t* scales,
+                               void* stream) {
+    gnf4_status st = check_act8_sizes(rows, K);
+    if (st != GNF4_OK || rows == 0) return st;
+    if ((st = check_act8_args(x, codes, scales)) != GNF4_OK) return st;
+    cudaError_t e = launch_quantize_act8(x, rows * K, codes, scales, reinterpret_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? GNF4_OK : cuda_fail(e, "quantize_act8 launch");
+}
+
+gnf4_status gnf4_dequantize_act8(const int8_t* codes, const uint8_t* scales, int64_t rows, int64_t K, void* out,
+                                 void* stream) {
+    gnf4_status st = check_act8_sizes(rows, K);
+    if (st != GNF4_OK || rows == 0) return st;
+    if ((st = check_act8_args(out, codes, scales)) != GNF4_OK) return st;
+    cudaError_t e = launch_dequantize_act8(codes, scales, rows * K, out, reinterpret_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? GNF4_OK : cuda_fail(e, "dequantize_act8 launch");
+}
+
+gnf4_status gnf4_swiglu_act8(const void* gate_up, int64_t R, int64_t I, void* out, int8_t* codes, uint8_t* scales,
+                             void* stream) {
+    gnf4_status st = check_swiglu_sizes(R, I, 32);
+    if (st != GNF4_OK || R == 0) return st;
+    if (!out) return fail(GNF4_ERR_INVALID_ARG, "null pointer argument");
+    if (!aligned16(out)) return fail(GNF4_ERR_MISALIGNED, "out must be 16-byte aligned");
+    if ((st = check_act8_args(gate_up, codes, scales)) != GNF4_OK) return st;
+    if ((st = check_device({out})) != GNF4_OK) return st;
+    cudaError_t e = launch_swiglu_act8(gate_up, R, I, out, codes, scales, reinterpret_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? GNF4_OK : cuda_fail(e, "swiglu_act8 launch");
+}
+
+gnf4_status gnf4_swiglu_backward(const void* grad_out, const void* gate_up, const int8_t* codes, const uint8_t* scales,
+                                 int64_t R, int64_t I, void* grad_gate_up, void* act, void* stream) {
+    gnf4_status st = check_swiglu_sizes(R, I, codes ? 32 : 8);
+    if (st != GNF4_OK || R == 0) return st;
+    if (!grad_out || !grad_gate_up) return fail(GNF4_ERR_INVALID_ARG, "null pointer argument");
+    if (gate_up ? (codes || scales) : !(codes && scales))
+        return fail(GNF4_ERR_INVALID_ARG, "give either gate_up or its checkpoint (codes and scales)");
+    if (!aligned16(grad_out) || !aligned16(gate_up) || !aligned16(grad_gate_up) || !aligned16(act) || !aligned8(codes))
+        return fail(GNF4_ERR_MISALIGNED, "bf16 rows must be 16-byte and codes 8-byte aligned");
+    if ((st = check_device({grad_out, gate_up, codes, scales, grad_gate_up, act})) != GNF4_OK) return st;
+    cudaError_t e = launch_swiglu_backward(grad_out, gate_up, codes, scales, R, I, grad_gate_up, act,
+                                           reinterpret_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? GNF4_OK : cuda_fail(e, "swiglu_backward launch");
+}
+
+gnf4_status gnf4_lora_apply(const void* base, const void* x, int dtype, const void* A, const void* B,
+                            const int64_t* adapter_offsets, const int32_t* row_token, const float* row_weight,
+                            const int32_t* row_dest, const float* scaling, int64_t L, int64_t r, int64_t N, int64_t K,
+                            int64_t R, int64_t T_in, int64_t T_out, void* out, float* h, int flags, void* stream) {
+    if (dtype != GNF4_DTYPE_BF16 && dtype != GNF4_DTYPE_F16)
+        return fail(GNF4_ERR_INVALID_ARG, "dtype must be GNF4_DTYPE_BF16 or GNF4_DTYPE_F16");
+    const LoraCommon c{A, B, adapter_offsets, row_token, row_dest, row_weight, scaling, L, r, N, K, R, T_in, T_out, flags};
+    gnf4_status st = check_lora_sizes(c);
+    if (st != GNF4_OK || R == 0) return st;
+    if ((st = check_lora_buffers(c)) != GNF4_OK) return st;
+    if (!x || !out) return fail(GNF4_ERR_INVALID_ARG, "null pointer argument");
+    if (!aligned16(x) || !aligned16(base) || !aligned16(out) || !aligned4(h))
+        return fail(GNF4_ERR_MISALIGNED, "x, base and out must be 16-byte and h 4-byte aligned");
+    if ((st = check_lora_device(c)) != GNF4_OK || (st = check_device({x, base, out, h})) != GNF4_OK) return st;
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    if ((flags & GNF4_CHECK) && (st = check_lora_rows(c, s)) != GNF4_OK) return st;
+    LoraRowsArgs a;
+    a.src = reinterpret_cast<const uint16_t*>(x);
+    a.src_row = row_token;
+    a.down = reinterpret_cast<const uint16_t*>(A);
+    a.up = reinterpret_cast<const uint16_t*>(B);
+    a.base = reinterpret_cast<const uint16_t*>(base);
+    a.out = reinterpret_cast<uint16_t*>(out);
+    a.dst_row = row_dest;
+    a.offsets = adapter_offsets;
+    a.weight = row_weight;
+    a.scaling = scaling;
+    a.mid = h;
+    a.R = R;
+    a.n_src = T_in;
+    a.n_dst = T_out;
+    a.L = (int)L;
+    a.r = (int)r;
+    a.C = (int)K;
+    a.O = (int)N;
+    cudaError_t e = launch_lora_rows(a, false, dtype == GNF4_DTYPE_F16, s);
+    return e == cudaSuccess ? GNF4_OK : cuda_fail(e, "lora_apply launch");
+}
+
+gnf4_status gnf4_lora_backward(const void* grad_out, const void* x, const int8_t* x_codes, const uint8_t* x_scales,
+                               const float* h, const void* A, const void* B, const int64_t* adapter_offsets,
+                               const int32_t* row_token, const float* row_weight, const int32_t* row_src,
+                               const float* scaling, int64_t L, int64_t r, int64_t N, int64_t K, int64_t R,
+                               int64_t T_in, int64_t T_g, const void* dx_base, void* dx, float* grad_h, void* dA,
+                               void* dB, int grad_dtype, int flags, void* stream) {
+    if (grad_dtype != GNF4_DTYPE_BF16 && grad_dtype != GNF4_DTYPE_F32)
+        return fail(GNF4_ERR_INVALID_ARG, "grad_dtype must be GNF4_DTYPE_BF16 or GNF4_DTYPE_F32");
+    const LoraCommon c{A, B, adapter_offsets, row_token, row_src, row_weight, scaling, L, r, N, K, R, T_in, T_g, flags};
+    gnf4_status st = check_lora_sizes(c);
+    if (st != GNF4_OK) return st;
+    if (x_codes && K % 32) return fail(GNF4_ERR_UNSUPPORTED_SHAPE, "a checkpoint of x needs K % 32 == 0");
+    if (!dB) return fail(GNF4_ERR_INVALID_ARG, "null pointer argument");
+    if (R > 0) {
+        if ((st = check_lora_buffers(c)) != GNF4_OK) return st;
+        if (!grad_out || !h || !grad_h || (dx_base && !dx)) return fail(GNF4_ERR_INVALID_ARG, "null pointer argument");
+        if ((st = check_lora_x(x, x_codes, x_scales, !dA)) != GNF4_OK) return st;
+    } else if (!adapter_offsets || !aligned8(adapter_offsets)) {
+        return fail(GNF4_ERR_INVALID_ARG, "adapter_offsets must be given, 8-byte aligned");
+    }
+    if (!aligned16(grad_out) || !aligned16(x) || !aligned8(x_codes) || !aligned16(dx_base) || !aligned16(dx) ||
+        !aligned4(h) || !aligned4(grad_h) || !aligned16(dA) || !aligned16(dB))
+        return fail(GNF4_ERR_MISALIGNED, "16-bit rows, dA and dB must be 16-byte, x_codes 8-byte, h and grad_h 4-byte aligned");
+    if ((st = check_lora_device(c)) != GNF4_OK) return st;
+    if ((st = check_device({grad_out, x, x_codes, x_scales, h, dx_base, dx, grad_h, dA, dB})) != GNF4_OK) return st;
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    if (R > 0) {
+        if ((flags & GNF4_CHECK) && (st = check_lora_rows(c, s)) != GNF4_OK) return st;
+        LoraRowsArgs a;
+        a.src = reinterpret_cast<const uint16_t*>(grad_out);
+        a.src_row = row_src;
+        a.down = reinterpret_cast<const uint16_t*>(B);
+        a.up = reinterpret_cast<const uint16_t*>(A);
+        a.base = reinterpret_cast<const uint16_t*>(dx_base);
+        a.out = reinterpret_cast<uint16_t*>(dx);
+        a.dst_row = nullptr;
+        a.offsets = adapter_offsets;
+        a.weight = row_weight;
+        a.scaling = scaling;
+        a.mid = grad_h;
+        a.R = R;
+        a.n_src = T_g;
+        a.n_dst = dx ? R : 0;                     // no dx: no row is written
+        a.L = (int)L;
+        a.r = (int)r;
+        a.C = (int)N;
+        a.O = (int)K;
+        cudaError_t e = launch_lora_rows(a, true, false, s);
+        if (e != cudaSuccess) return cuda_fail(e, "lora_backward launch");
+    }
+    LoraGradArgs q;
+    q.a = grad_a_side(grad_h, x, x_codes, x_scales, row_token, T_in, K, dA);
+    q.b.left = h;
+    q.b.right = reinterpret_cast<const uint16_t*>(grad_out);
+    q.b.codes = nullptr;
+    q.b.scales = nullptr;
+    q.b.row = row_src;
+    q.b.out = dB;
+    q.b.n = T_g;
+    q.b.C = (int)N;
+    q.b.factor = 1;
+    q.b.transposed = 1;
+    q.offsets = adapter_offsets;
+    q.weight = row_weight;
+    q.scaling = scaling;
+    q.R = R;
+    q.L = (int)L;
+    q.r = (int)r;
+    cudaError_t e = launch_lora_grads(q, grad_dtype == GNF4_DTYPE_F32, s);
+    return e == cudaSuccess ? GNF4_OK : cuda_fail(e, "lora_backward gradient launch");
+}
+
+gnf4_status gnf4_lora_grad_a(const float* grad_h, const void* x, const int8_t* x_codes, const uint8_t* x_scales,
+                             const int64_t* adapter_offsets, const int32_t* row_token, int64_t L, int64_t r, int64_t K,
+                             int64_t R, int64_t T_in, void* dA, int grad_dtype, int flags, void* stream) {
+    if (grad_dtype != GNF4_DTYPE_BF16 && grad_dtype != GNF4_DTYPE_F32)
+        return fail(GNF4_ERR_INVALID_ARG, "grad_dtype must be GNF4_DTYPE_BF16 or GNF4_DTYPE_F32");
+    // the projection's output side does not enter: N = 8 and R rows stand in for it in the common checks
+    const LoraCommon c{nullptr, nullptr, adapter_offsets, row_token, nullptr, nullptr, nullptr, L, r, 8, K, R, T_in, R, flags};
+    gnf4_status st = check_lora_sizes(c);
+    if (st != GNF4_OK) return st;
+    if (x_codes && K % 32) return fail(GNF4_ERR_UNSUPPORTED_SHAPE, "a checkpoint of x needs K % 32 == 0");
+    if (!dA || !adapter_offsets || (R > 0 && !grad_h)) return fail(GNF4_ERR_INVALID_ARG, "null pointer argument");
+    if (R > 0 && (st = check_lora_x(x, x_codes, x_scales, false)) != GNF4_OK) return st;
+    if (!aligned16(x) || !aligned8(x_codes) || !aligned4(grad_h) || !aligned16(dA) || !aligned8(adapter_offsets) ||
+        !aligned4(row_token))
+        return fail(GNF4_ERR_MISALIGNED, "x and dA must be 16-byte, x_codes and adapter_offsets 8-byte, grad_h and row_token 4-byte aligned");
+    if ((st = check_device({grad_h, x, x_codes, x_scales, adapter_offsets, row_token, dA})) != GNF4_OK) return st;
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    if (R > 0 && (flags & GNF4_CHECK) && (st = check_lora_rows(c, s)) != GNF4_OK) return st;
+    LoraGradArgs q;
+    std::memset(&q, 0, sizeof(q));
+    q.a = grad_a_side(grad_h, x, x_codes, x_scales, row_token, T_in, K, dA);
+    q.offsets = adapter_offsets;
+    q.R = R;
+    q.L = (int)L;
+    q.r = (int)r;
+    cudaError_t e = launch_lora_grads(q, grad_dtype == GNF4_DTYPE_F32, s);
+    return e == cudaSuccess ? GNF4_OK : cuda_fail(e, "lora_grad_a launch");
 }
 
 int gnf4_grouped_gemm_launches(int64_t R, int flags) {

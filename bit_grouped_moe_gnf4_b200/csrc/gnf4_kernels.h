@@ -57,6 +57,60 @@ cudaError_t launch_routing(const int32_t* ids, const float* weights, int64_t T, 
                            int64_t* offsets, int32_t* row_token, float* row_weight, int32_t* row_dest,
                            cudaStream_t s);
 
+// 8-bit activation checkpoints (n elements, a multiple of 32) and the SwiGLU's backward
+// (codes and scales instead of gate_up when that is null); sizes validated, nothing empty.
+cudaError_t launch_quantize_act8(const void* x, int64_t n, int8_t* codes, uint8_t* scales, cudaStream_t s);
+cudaError_t launch_dequantize_act8(const int8_t* codes, const uint8_t* scales, int64_t n, void* out, cudaStream_t s);
+cudaError_t launch_swiglu_act8(const void* gate_up, int64_t R, int64_t I, void* out, int8_t* codes, uint8_t* scales,
+                               cudaStream_t s);
+cudaError_t launch_swiglu_backward(const void* d_out, const void* gate_up, const int8_t* codes, const uint8_t* scales,
+                                   int64_t R, int64_t I, void* d_gate_up, void* again, cudaStream_t s);
+
+// The two chained products of a low-rank adapter over routed rows, on top of base:
+// mid[r] = down(e)^T src[src_row r] (C -> r), out[dst_row r] = base[dst_row r] + c_r up(e)^T mid[r]
+// (r -> O). Forward: down = A [L, r, C], up = B [L, O, r], mid without c_r. Backward: down =
+// B [L, C, r], up = A [L, r, O], mid times c_r.
+struct LoraRowsArgs {
+    const uint16_t* src;        // [n_src, C]
+    const int32_t* src_row;     // [R] or null
+    const uint16_t* down;
+    const uint16_t* up;
+    const uint16_t* base;       // [n_dst, O] or null (zeros); may be out
+    uint16_t* out;              // [n_dst, O]
+    const int32_t* dst_row;     // [R] or null
+    const int64_t* offsets;     // [L+1]
+    const float* weight;        // [R] or null
+    const float* scaling;       // [L] or null
+    float* mid;                 // [R, r] or null
+    int64_t R, n_src, n_dst;
+    int L, r, C, O;
+};
+cudaError_t launch_lora_rows(const LoraRowsArgs& a, bool bwd, bool f16, cudaStream_t s);
+
+// One of the two adapter gradients: sum over adapter e's rows of left[r, j] right[row r, n],
+// left times c_r where `factor`, stored [L, r, C] or (transposed) [L, C, r]
+struct LoraGradSide {
+    const float* left;          // [R, r]
+    const uint16_t* right;      // bf16 [n, C], or null: the checkpoint below
+    const int8_t* codes;        // [n, C]
+    const uint8_t* scales;      // [n, C/32]
+    const int32_t* row;         // [R] or null
+    void* out;                  // null: this gradient is not asked for
+    int64_t n;
+    int C, factor, transposed;
+};
+struct LoraGradArgs {
+    LoraGradSide a, b;          // dA (may read a checkpoint), dB
+    const int64_t* offsets;     // [L+1]
+    const float* weight;        // [R] or null
+    const float* scaling;       // [L] or null
+    int64_t R;
+    int L, r;
+};
+cudaError_t launch_lora_grads(const LoraGradArgs& a, bool f32, cudaStream_t s);
+cudaError_t launch_check_lora(const int64_t* offsets, int L, int64_t R, const int32_t* a, int64_t na, const int32_t* b,
+                              int64_t nb, const float* w, unsigned* status, cudaStream_t s);
+
 int device_sm_count();
 
 // The current CUDA device, clamped to [0, 64) for the per-device caches (kernel

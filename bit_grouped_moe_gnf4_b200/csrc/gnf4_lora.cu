@@ -1,0 +1,813 @@
+// Low-rank adapters beside a projection, for routed rows r sorted by adapter e:
+//   forward    h_r = A_e x[tok r],           out[dest r] = base[dest r] + c_r B_e h_r
+//   backward   g_r = c_r B_e^T dy[src r],    dx_r = base_dx_r + A_e^T g_r
+//              dA_e = sum_r g_r x[tok r]^T,  dB_e = sum_r c_r dy[src r] h_r^T
+// with c_r = scaling_e w_r. A [L, r, K], B [L, N, r].
+//
+// The rank is small, so every product is bound by the rows it streams (or, with few rows,
+// by the adapters' bytes and latency), not by the tensor pipe: warp-level MMAs fed straight
+// from 16-byte global loads, whose fragment layouts are reached by permuting the contraction
+// index and the output columns instead of passing the operands through shared memory.
+//
+// lora_rows_kernel does the two products of the forward, or the first two of the backward
+// (the same chain with A and B swapped and both read along their other axis), in one
+// launch: a cluster of CTAs owns a tile of 16 or 32 rows of one adapter; its warps split the
+// contraction of the first product, the partial sums meet in shared memory (and through
+// distributed shared memory when the cluster has more than one CTA), and then the warps
+// split the output columns of the second. x, base and out are touched once.
+//
+// lora_grads_kernel sums over an adapter's rows: a warp owns a slab of the gradient's
+// columns, rows are the MMA's contraction index.
+//
+// Rounding: sums are fp32. h (and g) enter the second product as two 16-bit terms (value
+// and remainder: about 17 significant bits, so that what the caller sees is the one
+// rounding of the output); for fp16 they are first scaled by a power of two per row, so
+// that neither term leaves the type's range. The gradient sums take two terms for bf16
+// results and three (24 bits) for fp32 results.
+#include <atomic>
+#include <climits>
+#include <cstdint>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+#include "gnf4_act8.cuh"
+#include "gnf4_kernels.h"
+
+namespace gnf4 {
+
+namespace {
+
+constexpr int kLoraThreads = 256;
+constexpr int kLoraWarps = kLoraThreads / 32;
+
+__device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
+    uint32_t d;
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
+    return d;
+}
+
+template <bool F16>
+__device__ __forceinline__ uint32_t pack16(float lo, float hi) {
+    if constexpr (F16) {
+        const __half2 h = __floats2half2_rn(lo, hi);
+        return *reinterpret_cast<const uint32_t*>(&h);
+    } else {
+        return pack_bf16x2(lo, hi);
+    }
+}
+
+template <bool F16>
+__device__ __forceinline__ float2 unpack16(uint32_t w) {
+    if constexpr (F16) return __half22float2(*reinterpret_cast<const __half2*>(&w));
+    else return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
+}
+
+template <bool F16>
+__device__ __forceinline__ void mma16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                      uint32_t b1) {
+    if constexpr (F16)
+        asm volatile(
+            "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};\n"
+            : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+            : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+    else
+        mma_bf16_16816(c, a0, a1, a2, a3, b0, b1);
+}
+
+// lane (g, t) holds row g, columns 2t, 2t+1 of an 8x8 matrix; afterwards rows 2t, 2t+1 of column g
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t v) {
+    uint32_t d;
+    asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(v));
+    return d;
+}
+
+__device__ __forceinline__ uint4 ldg16(const uint16_t* p) { return __ldg(reinterpret_cast<const uint4*>(p)); }
+__device__ __forceinline__ uint2 ldg8(const uint16_t* p) { return __ldg(reinterpret_cast<const uint2*>(p)); }
+
+// value = sum of TERMS bf16 (or fp16) numbers, each the rounding of what the ones before it
+// leave; a value that is not finite stays in the first
+template <int TERMS, bool F16>
+__device__ __forceinline__ void split_pair(float v0, float v1, uint32_t (&o)[TERMS]) {
+#pragma unroll
+    for (int i = 0; i < TERMS; ++i) {
+        o[i] = pack16<F16>(v0, v1);
+        const float2 f = unpack16<F16>(o[i]);
+        v0 = isfinite(f.x) ? v0 - f.x : 0.0f;
+        v1 = isfinite(f.y) ? v1 - f.y : 0.0f;
+    }
+}
+
+__device__ __forceinline__ uint32_t cluster_rank() {
+    uint32_t r;
+    asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ uint32_t cluster_size() {
+    uint32_t r;
+    asm("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire;" ::: "memory"); }
+// a float of another CTA's shared memory, at the address that `local` has in this CTA's
+__device__ __forceinline__ float ld_cluster(const float* local, uint32_t rank) {
+    uint32_t a;
+    float v;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_addr(local)), "r"(rank));
+    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(a) : "memory");
+    return v;
+}
+
+// rows of adapter e, kept inside [0, R] whatever the offsets hold
+__device__ __forceinline__ int64_t clamp_row(int64_t v, int64_t R) { return v < 0 ? 0 : v > R ? R : v; }
+
+struct Tile {
+    int e, rows;
+    int64_t row0;
+};
+
+// Tile `tile` of the list of all adapters' tiles of BM rows: each thread counts the tiles of
+// a run of neighbouring adapters, a block scan places them, and the thread whose run covers
+// the tile writes it down. s_tile->rows is 0 when the list is shorter.
+template <int BM>
+__device__ __forceinline__ void find_tile(const int64_t* offsets, int L, int64_t R, int tile, Tile* s_tile, int* s_warp) {
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int per = (L + kLoraThreads - 1) / kLoraThreads;
+    const int e0 = min(tid * per, L), e1 = min(e0 + per, L);
+    int mine = 0;
+    int64_t lo = e0 < e1 ? clamp_row(offsets[e0], R) : 0;
+    const int64_t first = lo;
+    for (int e = e0; e < e1; ++e) {
+        const int64_t hi = clamp_row(offsets[e + 1], R);
+        if (hi > lo) mine += (int)((hi - lo + BM - 1) / BM);
+        lo = hi;
+    }
+    int incl = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int u = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += u;
+    }
+    if (lane == 31) s_warp[warp] = incl;
+    if (tid == 0) s_tile->rows = 0;
+    __syncthreads();
+    for (int w = 0; w < warp; ++w) incl += s_warp[w];
+    int at = incl - mine;
+    if (tile >= at && tile < incl) {
+        lo = first;
+        for (int e = e0; e < e1; ++e) {
+            const int64_t hi = clamp_row(offsets[e + 1], R);
+            const int n = hi > lo ? (int)((hi - lo + BM - 1) / BM) : 0;
+            if (tile < at + n) {
+                s_tile->e = e;
+                s_tile->row0 = lo + (int64_t)(tile - at) * BM;
+                s_tile->rows = (int)min((int64_t)BM, hi - s_tile->row0);
+                break;
+            }
+            at += n;
+            lo = hi;
+        }
+    }
+    __syncthreads();
+}
+
+template <int RP>
+struct RowsShape {
+    static constexpr int kPlaneStride = RP + (RP >= 64 ? 32 : 0);    // 16-bit elements; conflict-free fragment loads
+    static constexpr int kRedStride = RP + 8;                        // floats
+    static constexpr int kSub = RP <= 32 ? 2 : 1;                    // 32-column groups a warp holds at once
+};
+
+template <int RP, int MT>
+constexpr size_t rows_smem() {
+    using S = RowsShape<RP>;
+    return sizeof(float) * (size_t)kLoraWarps * 16 * MT * S::kRedStride         // the warps' partial sums
+           + sizeof(float) * (size_t)16 * MT * S::kRedStride                    // their sum
+           + sizeof(uint16_t) * (size_t)2 * 16 * MT * S::kPlaneStride           // its two 16-bit terms
+           + sizeof(float) * (size_t)16 * MT;                                   // output factor of each row
+}
+
+// RP: rank padded to 16, 32, 64 or 128; MT: 16-row MMA tiles a CTA; BWD: the backward's chain
+// (first factor [L, C, r], second [L, r, O]) instead of the forward's ([L, r, C], [L, O, r])
+template <int RP, int MT, bool BWD, bool F16>
+__global__ void __launch_bounds__(kLoraThreads, RP <= 32 ? 2 : 1) lora_rows_kernel(const LoraRowsArgs p) {
+    using S = RowsShape<RP>;
+    constexpr int BM = 16 * MT, NT = RP / 8;
+    extern __shared__ __align__(16) uint8_t smem[];
+    float* s_red = reinterpret_cast<float*>(smem);
+    float* s_sum = s_red + (size_t)kLoraWarps * BM * S::kRedStride;
+    uint16_t* s_plane = reinterpret_cast<uint16_t*>(s_sum + (size_t)BM * S::kRedStride);
+    float* s_fac = reinterpret_cast<float*>(s_plane + (size_t)2 * BM * S::kPlaneStride);
+    __shared__ Tile s_tile;
+    __shared__ int s_warp[kLoraWarps];
+
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int g = lane >> 2, t = lane & 3;
+    const int CS = (int)cluster_size(), crank = (int)cluster_rank();
+    find_tile<BM>(p.offsets, p.L, p.R, (int)(blockIdx.x / CS), &s_tile, s_warp);
+    const int rows = s_tile.rows, e = s_tile.e;
+    const int64_t row0 = s_tile.row0;
+    if (rows == 0) return;                       // the same in every CTA of the cluster
+
+    // ---- first product: [BM, C] x [C, r], the contraction split over all warps of the cluster
+    {
+        const uint16_t* src[MT][2];
+#pragma unroll
+        for (int m = 0; m < MT; ++m)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const int local = 16 * m + 8 * h + g;
+                src[m][h] = nullptr;
+                if (local < rows) {
+                    const int64_t r = row0 + local;
+                    const int64_t at = p.src_row ? (int64_t)__ldg(p.src_row + r) : r;
+                    if (at >= 0 && at < p.n_src) src[m][h] = p.src + at * p.C + 8 * t;
+                }
+            }
+        float acc[MT][NT][4];
+#pragma unroll
+        for (int m = 0; m < MT; ++m)
+#pragma unroll
+            for (int c = 0; c < NT; ++c)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) acc[m][c][j] = 0.0f;
+        const uint16_t* down = p.down + (int64_t)e * p.r * p.C;
+        const int steps = (p.C + 31) / 32, parts = CS * kLoraWarps, part = crank * kLoraWarps + warp;
+        const int st0 = (int)((int64_t)steps * part / parts), st1 = (int)((int64_t)steps * (part + 1) / parts);
+#pragma unroll 2
+        for (int st = st0; st < st1; ++st) {
+            const int k0 = 32 * st;
+            uint4 a[MT][2];
+#pragma unroll
+            for (int m = 0; m < MT; ++m)
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+                    a[m][h] = src[m][h] && k0 + 8 * t < p.C ? ldg16(src[m][h] + k0) : make_uint4(0u, 0u, 0u, 0u);
+            // b[c]: this lane's contraction indices k0 + 8t .. 8t+7 of rank tile c, as four pairs
+            uint4 b[NT];
+            if constexpr (!BWD) {
+                // rank row 8c + g, 16 bytes along the contraction
+#pragma unroll
+                for (int c = 0; c < NT; ++c) {
+                    const int j = 8 * c + g;
+                    b[c] = j < p.r && k0 + 8 * t < p.C ? ldg16(down + (int64_t)j * p.C + k0 + 8 * t)
+                                                       : make_uint4(0u, 0u, 0u, 0u);
+                }
+            } else {
+                // pair q of the fragment: contraction rows k0 + 8 (g>>1) + 2q + (g&1), rank along
+                // the lanes' t; a transposed 8x8 matrix gives each lane its two rows of one column
+                constexpr int V = RP >= 32 ? 4 : 2;            // rank tiles in one vector
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    const int k = k0 + 8 * (g >> 1) + 2 * q + (g & 1);
+#pragma unroll
+                    for (int v = 0; v < NT / V; ++v) {
+                        const int j = 8 * V * v + 2 * V * t;
+                        uint32_t w[4] = {0u, 0u, 0u, 0u};
+                        if (k < p.C && j < p.r) {
+                            const uint16_t* at = down + (int64_t)k * p.r + j;
+                            if constexpr (V == 4) {
+                                const uint4 x = ldg16(at);
+                                w[0] = x.x, w[1] = x.y, w[2] = x.z, w[3] = x.w;
+                            } else {
+                                const uint2 x = ldg8(at);
+                                w[0] = x.x, w[1] = x.y;
+                            }
+                        }
+#pragma unroll
+                        for (int i = 0; i < V; ++i) {
+                            const uint32_t f = transpose8x8(w[i]);
+                            uint4& d = b[V * v + i];
+                            if (q == 0) d.x = f;
+                            else if (q == 1) d.y = f;
+                            else if (q == 2) d.z = f;
+                            else d.w = f;
+                        }
+                    }
+                }
+            }
+#pragma unroll
+            for (int m = 0; m < MT; ++m)
+#pragma unroll
+                for (int c = 0; c < NT; ++c) {
+                    mma16<F16>(acc[m][c], a[m][0].x, a[m][1].x, a[m][0].y, a[m][1].y, b[c].x, b[c].y);
+                    mma16<F16>(acc[m][c], a[m][0].z, a[m][1].z, a[m][0].w, a[m][1].w, b[c].z, b[c].w);
+                }
+        }
+        // partial sums: tile c, column index n of the MMA is rank 8c + n (forward), or
+        // 8 V (c / V) + 2 V (n >> 1) + 2 (c % V) + (n & 1) (backward)
+        float* mine = s_red + (size_t)warp * BM * S::kRedStride;
+#pragma unroll
+        for (int m = 0; m < MT; ++m)
+#pragma unroll
+            for (int c = 0; c < NT; ++c) {
+                int j = 8 * c + 2 * t;
+                if constexpr (BWD) {
+                    constexpr int V = RP >= 32 ? 4 : 2;
+                    j = 8 * V * (c / V) + 2 * V * t + 2 * (c % V);
+                }
+                *reinterpret_cast<float2*>(mine + (16 * m + g) * S::kRedStride + j) = make_float2(acc[m][c][0], acc[m][c][1]);
+                *reinterpret_cast<float2*>(mine + (16 * m + 8 + g) * S::kRedStride + j) = make_float2(acc[m][c][2], acc[m][c][3]);
+            }
+    }
+    __syncthreads();
+    if (CS > 1) {
+        for (int i = tid; i < BM * RP; i += kLoraThreads) {
+            const int at = (i / RP) * S::kRedStride + i % RP;
+            float v = 0.0f;
+#pragma unroll
+            for (int w = 0; w < kLoraWarps; ++w) v += s_red[(size_t)w * BM * S::kRedStride + at];
+            s_sum[at] = v;
+        }
+        cluster_arrive();
+        cluster_wait();
+    }
+    // ---- the sums, their 16-bit terms and each row's output factor (a warp per row)
+    const float scal = p.scaling ? __ldg(p.scaling + e) : 1.0f;
+    for (int local = warp; local < BM; local += kLoraWarps) {
+        constexpr int PER = (RP + 31) / 32;
+        float v[PER];
+        const int64_t r = row0 + local;
+        float fac = scal;
+        if (local < rows && p.weight) fac *= __ldg(p.weight + r);
+        float big = 0.0f;
+#pragma unroll
+        for (int i = 0; i < PER; ++i) {
+            const int j = 32 * i + lane;
+            v[i] = 0.0f;
+            if (j < p.r && local < rows) {
+                const int at = local * S::kRedStride + j;
+                if (CS > 1) {
+                    for (int c = 0; c < CS; ++c) v[i] += ld_cluster(s_sum + at, c);
+                } else {
+#pragma unroll
+                    for (int w = 0; w < kLoraWarps; ++w) v[i] += s_red[(size_t)w * BM * S::kRedStride + at];
+                }
+                if (BWD) v[i] *= fac;
+                if (crank == 0 && p.mid) p.mid[r * p.r + j] = v[i];
+            }
+            big = fmaxf(big, fabsf(v[i]));
+        }
+        if (BWD) fac = 1.0f;
+        if constexpr (F16) {
+            // the row's largest value to [1, 2): both terms stay normal or fall below 2^-24 of it
+#pragma unroll
+            for (int o = 16; o; o >>= 1) big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, o));
+            const uint32_t ex = __float_as_uint(big) >> 23;
+            if (ex > 0u && ex < 254u) {
+                const float down = __uint_as_float((254u - ex) << 23);
+#pragma unroll
+                for (int i = 0; i < PER; ++i) v[i] *= down;
+                fac *= __uint_as_float(ex << 23);
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < PER; ++i) {
+            const int j = 32 * i + lane;
+            if (j < RP) {
+                uint32_t o[2];
+                split_pair<2, F16>(v[i], 0.0f, o);
+                s_plane[(size_t)local * S::kPlaneStride + j] = (uint16_t)o[0];
+                s_plane[(size_t)(BM + local) * S::kPlaneStride + j] = (uint16_t)o[1];
+            }
+        }
+        if (lane == 0) s_fac[local] = fac;
+    }
+    if (CS > 1) cluster_arrive();                // this CTA has read its peers' sums; they may not leave before
+    __syncthreads();
+
+    // ---- second product: [BM, r] x [r, O] on top of base, the columns split over all warps
+    {
+        constexpr int KS = RP / 16, SUB = S::kSub;
+        constexpr int G = RP >= 32 ? 2 : 1;       // MMA steps that share one vector of the rank
+        const uint16_t* up = p.up + (int64_t)e * p.r * p.O;
+        int64_t dst[MT][2];
+        float fac[MT][2];
+#pragma unroll
+        for (int m = 0; m < MT; ++m)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const int local = 16 * m + 8 * h + g;
+                dst[m][h] = -1;
+                fac[m][h] = s_fac[local];
+                if (local < rows) {
+                    const int64_t r = row0 + local;
+                    const int64_t at = p.dst_row ? (int64_t)__ldg(p.dst_row + r) : r;
+                    if (at >= 0 && at < p.n_dst) dst[m][h] = at * p.O + 8 * t;
+                }
+            }
+        const int slabs = (p.O + 32 * SUB - 1) / (32 * SUB);
+        for (int slab = crank * kLoraWarps + warp; slab < slabs; slab += CS * kLoraWarps) {
+            const int n0 = slab * 32 * SUB;
+            uint4 bs[MT][2][SUB];
+#pragma unroll
+            for (int m = 0; m < MT; ++m)
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+#pragma unroll
+                    for (int s = 0; s < SUB; ++s)
+                        bs[m][h][s] = dst[m][h] >= 0 && p.base && n0 + 32 * s + 8 * t < p.O
+                                          ? *reinterpret_cast<const uint4*>(p.base + dst[m][h] + n0 + 32 * s)
+                                          : make_uint4(0u, 0u, 0u, 0u);
+            // b[s][c][q]: column n0 + 32 s + 4 g + c; the rank indices of step q held by this lane are
+            // 4t .. 4t+3 (RP = 16) or 32 (q >> 1) + 8t + 4 (q & 1) + 0..3
+            uint2 b[SUB][4][KS];
+#pragma unroll
+            for (int s = 0; s < SUB; ++s) {
+                const int col = n0 + 32 * s + 4 * g;
+                const bool in = col < p.O;
+                if constexpr (!BWD) {
+#pragma unroll
+                    for (int c = 0; c < 4; ++c)
+#pragma unroll
+                        for (int q = 0; q < KS; q += G) {
+                            const int j = 16 * q + 4 * G * t;
+                            b[s][c][q] = make_uint2(0u, 0u);
+                            if constexpr (G == 2) b[s][c][q + 1] = make_uint2(0u, 0u);
+                            if (in && j < p.r) {
+                                const uint16_t* at = up + (int64_t)(col + c) * p.r + j;
+                                if constexpr (G == 2) {
+                                    const uint4 v = ldg16(at);
+                                    b[s][c][q] = make_uint2(v.x, v.y);
+                                    b[s][c][q + 1] = make_uint2(v.z, v.w);
+                                } else {
+                                    b[s][c][q] = ldg8(at);
+                                }
+                            }
+                        }
+                } else {
+#pragma unroll
+                    for (int q = 0; q < KS; ++q) {
+                        const int j = 16 * G * (q / G) + 4 * G * t + 4 * (q % G);
+                        uint2 v[4];
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            v[i] = in && j + i < p.r ? ldg8(up + (int64_t)(j + i) * p.O + col) : make_uint2(0u, 0u);
+                        b[s][0][q] = make_uint2(prmt(v[0].x, v[1].x, 0x5410u), prmt(v[2].x, v[3].x, 0x5410u));
+                        b[s][1][q] = make_uint2(prmt(v[0].x, v[1].x, 0x7632u), prmt(v[2].x, v[3].x, 0x7632u));
+                        b[s][2][q] = make_uint2(prmt(v[0].y, v[1].y, 0x5410u), prmt(v[2].y, v[3].y, 0x5410u));
+                        b[s][3][q] = make_uint2(prmt(v[0].y, v[1].y, 0x7632u), prmt(v[2].y, v[3].y, 0x7632u));
+                    }
+                }
+            }
+#pragma unroll
+            for (int m = 0; m < MT; ++m) {
+                float acc[SUB][4][4];
+#pragma unroll
+                for (int s = 0; s < SUB; ++s)
+#pragma unroll
+                    for (int c = 0; c < 4; ++c)
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) acc[s][c][j] = 0.0f;
+#pragma unroll
+                for (int term = 0; term < 2; ++term) {
+                    const uint16_t* plane = s_plane + (size_t)(term * BM + 16 * m + g) * S::kPlaneStride;
+#pragma unroll
+                    for (int q = 0; q < KS; q += G) {
+                        uint2 a0[G], a1[G];
+                        const uint16_t* at = plane + 16 * q + 4 * G * t;
+                        if constexpr (G == 2) {
+                            const uint4 x = *reinterpret_cast<const uint4*>(at);
+                            const uint4 y = *reinterpret_cast<const uint4*>(at + 8 * S::kPlaneStride);
+                            a0[0] = make_uint2(x.x, x.y), a0[1] = make_uint2(x.z, x.w);
+                            a1[0] = make_uint2(y.x, y.y), a1[1] = make_uint2(y.z, y.w);
+                        } else {
+                            a0[0] = *reinterpret_cast<const uint2*>(at);
+                            a1[0] = *reinterpret_cast<const uint2*>(at + 8 * S::kPlaneStride);
+                        }
+#pragma unroll
+                        for (int i = 0; i < G; ++i)
+#pragma unroll
+                            for (int s = 0; s < SUB; ++s)
+#pragma unroll
+                                for (int c = 0; c < 4; ++c)
+                                    mma16<F16>(acc[s][c], a0[i].x, a1[i].x, a0[i].y, a1[i].y, b[s][c][q + i].x,
+                                               b[s][c][q + i].y);
+                    }
+                }
+                // lane (g, t): columns 8t + 4 i + c of each group in acc[s][c][2h + i]
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+#pragma unroll
+                    for (int s = 0; s < SUB; ++s) {
+                        if (dst[m][h] < 0 || n0 + 32 * s + 8 * t >= p.O) continue;
+                        const float f = fac[m][h];
+                        const uint32_t bw[4] = {bs[m][h][s].x, bs[m][h][s].y, bs[m][h][s].z, bs[m][h][s].w};
+                        uint32_t o[4];
+#pragma unroll
+                        for (int i = 0; i < 2; ++i)
+#pragma unroll
+                            for (int c = 0; c < 4; c += 2) {
+                                const float2 v = unpack16<F16>(bw[2 * i + c / 2]);
+                                o[2 * i + c / 2] = pack16<F16>(fmaf(f, acc[s][c][2 * h + i], v.x),
+                                                               fmaf(f, acc[s][c + 1][2 * h + i], v.y));
+                            }
+                        *reinterpret_cast<uint4*>(p.out + dst[m][h] + n0 + 32 * s) = make_uint4(o[0], o[1], o[2], o[3]);
+                    }
+            }
+        }
+    }
+    if (CS > 1) cluster_wait();
+}
+
+template <int RP, int MT, bool BWD, bool F16>
+cudaError_t launch_rows_t(const LoraRowsArgs& a, cudaStream_t s) {
+    constexpr int BM = 16 * MT;
+    constexpr size_t smem = rows_smem<RP, MT>();
+    static std::atomic<bool> attr_set[64];           // per device: dynamic shared memory opted in
+    const int dev = current_device();
+    if (!attr_set[dev].load(std::memory_order_acquire)) {
+        const cudaError_t e = cudaFuncSetAttribute(lora_rows_kernel<RP, MT, BWD, F16>,
+                                                   cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        if (e != cudaSuccess) return e;
+        attr_set[dev].store(true, std::memory_order_release);
+    }
+    // at most one partial tile for every adapter that has a row
+    const int64_t active = a.R < a.L ? a.R : a.L;
+    const int64_t tiles = active + (a.R - active) / BM;
+    int cs = 1;
+    while (cs < 8 && tiles * cs * 2 <= 2 * (int64_t)device_sm_count()) cs *= 2;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(tiles * cs));
+    cfg.blockDim = dim3(kLoraThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim.x = (unsigned)cs;
+    at[0].val.clusterDim.y = 1;
+    at[0].val.clusterDim.z = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, lora_rows_kernel<RP, MT, BWD, F16>, a);
+}
+
+template <int RP, int MT>
+cudaError_t launch_rows_m(const LoraRowsArgs& a, bool bwd, bool f16, cudaStream_t s) {
+    if (bwd) return launch_rows_t<RP, MT, true, false>(a, s);
+    return f16 ? launch_rows_t<RP, MT, false, true>(a, s) : launch_rows_t<RP, MT, false, false>(a, s);
+}
+
+template <int RP>
+cudaError_t launch_rows_r(const LoraRowsArgs& a, bool bwd, bool f16, cudaStream_t s) {
+    const int64_t active = a.R < a.L ? a.R : a.L;
+    return a.R >= 24 * active ? launch_rows_m<RP, 2>(a, bwd, f16, s) : launch_rows_m<RP, 1>(a, bwd, f16, s);
+}
+
+// ---------------------------------------------------------------------------
+// gradients of the adapters
+// ---------------------------------------------------------------------------
+template <int RP>
+struct GradShape {
+    static constexpr int CT = RP <= 32 ? 8 : 4;      // MMA column tiles of a warp's slab
+    static constexpr int SC = 8 * CT;                // its columns
+    static constexpr int MT = RP / 16;
+    static constexpr int kStride = SC + 4;           // floats of a row of the sum in shared memory
+};
+
+template <int RP>
+constexpr size_t grads_smem() {
+    return sizeof(float) * (size_t)kLoraWarps * RP * GradShape<RP>::kStride;
+}
+
+// One gradient of one adapter, `left` [R, r] fp32 (times the row's factor) against the rows
+// of `right` [*, C]: sum_r left[r, j] right[row r, n]. CTA: WC = 8 / WR slabs of columns, the
+// adapter's rows dealt out 16 at a time to WR warps of each of the cluster's CTAs.
+template <int RP, int WR, int TERMS, bool Q8>
+__device__ __forceinline__ void grad_body(const LoraGradArgs& p, const LoraGradSide& d, int e, int slab0, float* s_red) {
+    using S = GradShape<RP>;
+    constexpr int CT = S::CT, MT = S::MT, WC = kLoraWarps / WR;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int g = lane >> 2, t = lane & 3;
+    const int wc = warp % WC, wr = warp / WC;
+    const int CS = (int)cluster_size(), crank = (int)cluster_rank();
+    const int col = (slab0 + wc) * S::SC + CT * g;       // first of this lane's CT columns of every row
+    const bool in = col < d.C;
+    const int64_t lo = clamp_row(p.offsets[e], p.R), hi = clamp_row(p.offsets[e + 1], p.R);
+    const float scal = d.factor && p.scaling ? __ldg(p.scaling + e) : 1.0f;
+
+    float acc[MT][CT][4];
+#pragma unroll
+    for (int m = 0; m < MT; ++m)
+#pragma unroll
+        for (int c = 0; c < CT; ++c)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) acc[m][c][j] = 0.0f;
+
+    for (int64_t base = lo + 16 * (wr + (int64_t)WR * crank); base < hi; base += 16 * WR * CS) {
+        // this lane's four contraction rows: base + 4t .. 4t+3
+        uint32_t x[4][CT / 2];
+        float fac[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int64_t r = base + 4 * t + i;
+#pragma unroll
+            for (int w = 0; w < CT / 2; ++w) x[i][w] = 0u;
+            fac[i] = 0.0f;
+            if (r < hi) {
+                fac[i] = d.factor && p.weight ? scal * __ldg(p.weight + r) : scal;
+                const int64_t at = d.row ? (int64_t)__ldg(d.row + r) : r;
+                if (in && at >= 0 && at < d.n) {
+                    if constexpr (Q8) {
+                        const float step = act8_step(__ldg(d.scales + at * (d.C / 32) + (col >> 5)));
+                        uint2 q;
+                        if constexpr (CT == 8) q = __ldg(reinterpret_cast<const uint2*>(d.codes + at * d.C + col));
+                        else q = make_uint2(__ldg(reinterpret_cast<const uint32_t*>(d.codes + at * d.C + col)), 0u);
+                        float f[8];
+                        act8_values(q, step, f);
+#pragma unroll
+                        for (int w = 0; w < CT / 2; ++w) x[i][w] = pack_bf16x2(f[2 * w], f[2 * w + 1]);
+                    } else if constexpr (CT == 8) {
+                        const uint4 v = ldg16(d.right + at * d.C + col);
+                        x[i][0] = v.x, x[i][1] = v.y, x[i][2] = v.z, x[i][3] = v.w;
+                    } else {
+                        const uint2 v = ldg8(d.right + at * d.C + col);
+                        x[i][0] = v.x, x[i][1] = v.y;
+                    }
+                }
+            }
+        }
+        uint32_t a[MT][4][TERMS];
+#pragma unroll
+        for (int m = 0; m < MT; ++m)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const int j = 16 * m + 8 * h + g;
+                float v[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int64_t r = base + 4 * t + i;
+                    v[i] = r < hi && j < p.r ? fac[i] * __ldg(d.left + r * p.r + j) : 0.0f;
+                }
+                uint32_t o[TERMS];
+                split_pair<TERMS, false>(v[0], v[1], o);
+#pragma unroll
+                for (int q = 0; q < TERMS; ++q) a[m][h][q] = o[q];
+                split_pair<TERMS, false>(v[2], v[3], o);
+#pragma unroll
+                for (int q = 0; q < TERMS; ++q) a[m][2 + h][q] = o[q];
+            }
+#pragma unroll
+        for (int c = 0; c < CT; ++c) {
+            const uint32_t sel = (c & 1) ? 0x7632u : 0x5410u;
+            const uint32_t b0 = prmt(x[0][c / 2], x[1][c / 2], sel), b1 = prmt(x[2][c / 2], x[3][c / 2], sel);
+#pragma unroll
+            for (int m = 0; m < MT; ++m)
+#pragma unroll
+                for (int q = 0; q < TERMS; ++q)
+                    mma_bf16_16816(acc[m][c], a[m][0][q], a[m][1][q], a[m][2][q], a[m][3][q], b0, b1);
+        }
+    }
+    // MMA tile c, column index n of the accumulators is slab column CT n + c
+    float* mine = s_red + (size_t)warp * RP * S::kStride;
+#pragma unroll
+    for (int m = 0; m < MT; ++m)
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int c = 0; c < CT; ++c)
+#pragma unroll
+                for (int i = 0; i < 2; ++i)
+                    mine[(16 * m + 8 * h + g) * S::kStride + CT * (2 * t + i) + c] = acc[m][c][2 * h + i];
+    __syncthreads();
+    if (WR > 1) {
+        for (int i = tid; i < WC * RP * S::SC; i += kLoraThreads) {
+            const int w = i / (RP * S::SC), at = (i / S::SC % RP) * S::kStride + i % S::SC;
+            float v = s_red[(size_t)w * RP * S::kStride + at];
+#pragma unroll
+            for (int q = 1; q < WR; ++q) v += s_red[(size_t)(q * WC + w) * RP * S::kStride + at];
+            s_red[(size_t)w * RP * S::kStride + at] = v;
+        }
+        __syncthreads();
+    }
+    if (CS > 1) {
+        cluster_arrive();
+        cluster_wait();
+    }
+    // the cluster's CTAs share the elements out
+    const int share = (WC * RP * S::SC + CS - 1) / CS;
+    const int i1 = min((crank + 1) * share, WC * RP * S::SC);
+    for (int i = crank * share + tid; i < i1; i += kLoraThreads) {
+        const int w = i / (RP * S::SC), q = i % (RP * S::SC);
+        // consecutive threads along the gradient's contiguous axis: its columns (dA) or the rank (dB)
+        const int j = d.transposed ? q % RP : q / S::SC, n = d.transposed ? q / RP : q % S::SC;
+        const int c = (slab0 + w) * S::SC + n;
+        if (j >= p.r || c >= d.C) continue;
+        const float* at = s_red + (size_t)w * RP * S::kStride + j * S::kStride + n;
+        float v = 0.0f;
+        if (CS > 1)
+            for (int k = 0; k < CS; ++k) v += ld_cluster(at, k);
+        else
+            v = *at;
+        const int64_t o = (int64_t)e * p.r * d.C + (d.transposed ? (int64_t)c * p.r + j : (int64_t)j * d.C + c);
+        if (TERMS == 3) reinterpret_cast<float*>(d.out)[o] = v;
+        else reinterpret_cast<uint16_t*>(d.out)[o] = f32_to_bf16_rne(v);
+    }
+    if (CS > 1) {
+        cluster_arrive();
+        cluster_wait();
+    }
+}
+
+// CTAs (or clusters) of one adapter for one gradient; none for a gradient that is not asked for
+__host__ __device__ __forceinline__ int grad_items(const LoraGradSide& d, int cols) {
+    return d.out ? (d.C + cols - 1) / cols : 0;
+}
+
+template <int RP, int WR, int TERMS, bool Q8>
+__global__ void __launch_bounds__(kLoraThreads, RP <= 16 ? 2 : 1) lora_grads_kernel(const LoraGradArgs p) {
+    extern __shared__ __align__(16) float s_red[];
+    constexpr int WC = kLoraWarps / WR;
+    const int item = (int)(blockIdx.x / cluster_size());
+    const int na = grad_items(p.a, GradShape<RP>::SC * WC), nb = grad_items(p.b, GradShape<RP>::SC * WC);
+    const int e = item / (na + nb), i = item % (na + nb);
+    if (i < na) grad_body<RP, WR, TERMS, Q8>(p, p.a, e, i * WC, s_red);
+    else grad_body<RP, WR, TERMS, false>(p, p.b, e, (i - na) * WC, s_red);
+}
+
+template <int RP, int WR, int TERMS, bool Q8>
+cudaError_t launch_grads_t(const LoraGradArgs& a, int cs, cudaStream_t s) {
+    constexpr size_t smem = grads_smem<RP>();
+    static std::atomic<bool> attr_set[64];
+    const int dev = current_device();
+    if (!attr_set[dev].load(std::memory_order_acquire)) {
+        const cudaError_t e = cudaFuncSetAttribute(lora_grads_kernel<RP, WR, TERMS, Q8>,
+                                                   cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        if (e != cudaSuccess) return e;
+        attr_set[dev].store(true, std::memory_order_release);
+    }
+    constexpr int cols = GradShape<RP>::SC * (kLoraWarps / WR);
+    const int64_t items = (int64_t)a.L * (grad_items(a.a, cols) + grad_items(a.b, cols));
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(items * cs));
+    cfg.blockDim = dim3(kLoraThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim.x = (unsigned)cs;
+    at[0].val.clusterDim.y = 1;
+    at[0].val.clusterDim.z = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, lora_grads_kernel<RP, WR, TERMS, Q8>, a);
+}
+
+template <int RP, int WR>
+cudaError_t launch_grads_w(const LoraGradArgs& a, bool f32, int cs, cudaStream_t s) {
+    if (a.a.codes) return f32 ? launch_grads_t<RP, WR, 3, true>(a, cs, s) : launch_grads_t<RP, WR, 2, true>(a, cs, s);
+    return f32 ? launch_grads_t<RP, WR, 3, false>(a, cs, s) : launch_grads_t<RP, WR, 2, false>(a, cs, s);
+}
+
+template <int RP>
+cudaError_t launch_grads_r(const LoraGradArgs& a, bool f32, cudaStream_t s) {
+    // warps along the rows of an adapter until each has about 128 of them
+    const int64_t active = a.R < a.L ? (a.R > 0 ? a.R : 1) : a.L;
+    const int64_t avg = (a.R + active - 1) / active;
+    if (avg <= 512) return launch_grads_w<RP, 2>(a, f32, 1, s);
+    int cs = 1;
+    while (cs < 8 && avg > 1024 * cs) cs *= 2;
+    return launch_grads_w<RP, 8>(a, f32, cs, s);
+}
+
+// bits: 1 offsets decrease or leave [0, R], 2 offsets[0] != 0, 4 and 8 a row index of the rows
+// that exist is out of range, 16 a weight that is not finite
+__global__ void check_lora_kernel(const int64_t* offsets, int L, int64_t R, const int32_t* a, int64_t na,
+                                  const int32_t* b, int64_t nb, const float* w, unsigned* status) {
+    unsigned bad = 0;
+    const int64_t tid = (int64_t)blockIdx.x * blockDim.x + threadIdx.x, stride = (int64_t)gridDim.x * blockDim.x;
+    for (int64_t e = tid; e < L; e += stride)
+        if (offsets[e + 1] < offsets[e] || offsets[e + 1] > R) bad |= 1u;
+    if (tid == 0 && offsets[0] != 0) bad |= 2u;
+    const int64_t n = clamp_row(offsets[L], R);
+    for (int64_t r = tid; r < n; r += stride) {
+        if (a && (a[r] < 0 || a[r] >= na)) bad |= 4u;
+        if (b && (b[r] < 0 || b[r] >= nb)) bad |= 8u;
+        if (w && !isfinite(w[r])) bad |= 16u;
+    }
+    if (bad) atomicOr(status, bad);
+}
+
+}  // namespace
+
+cudaError_t launch_lora_rows(const LoraRowsArgs& a, bool bwd, bool f16, cudaStream_t s) {
+    if (a.r <= 16) return launch_rows_r<16>(a, bwd, f16, s);
+    if (a.r <= 32) return launch_rows_r<32>(a, bwd, f16, s);
+    if (a.r <= 64) return launch_rows_r<64>(a, bwd, f16, s);
+    return launch_rows_r<128>(a, bwd, f16, s);
+}
+
+cudaError_t launch_lora_grads(const LoraGradArgs& a, bool f32, cudaStream_t s) {
+    if (a.r <= 16) return launch_grads_r<16>(a, f32, s);
+    if (a.r <= 32) return launch_grads_r<32>(a, f32, s);
+    if (a.r <= 64) return launch_grads_r<64>(a, f32, s);
+    return launch_grads_r<128>(a, f32, s);
+}
+
+cudaError_t launch_check_lora(const int64_t* offsets, int L, int64_t R, const int32_t* a, int64_t na, const int32_t* b,
+                              int64_t nb, const float* w, unsigned* status, cudaStream_t s) {
+    check_lora_kernel<<<64, 256, 0, s>>>(offsets, L, R, a, na, b, nb, w, status);
+    return cudaGetLastError();
+}
+
+}  // namespace gnf4

@@ -356,6 +356,141 @@ gnf4_status gnf4_combine_topk(const void* y, int64_t R, int64_t N, const int32_t
                               void* stream);
 
 /*
+ * 8-bit activation checkpoints: what a training step keeps of its activations for the
+ * backward pass, at 1 + 1/32 bytes an element instead of 2. OCP MXINT8: int8 elements with
+ * one e8m0 scale per 32 elements along the row. For a block of 32 bf16 values
+ *   scales[b] = the exponent field (bits 7..14) of the largest magnitude, that is
+ *               floor(log2 max|x|) + 127, and 0 if that is zero or subnormal
+ *   codes[i]  = clamp( rne( x[i] * 2^(133 - scales[b]) ), -127, 127 )
+ * and a code stands for codes[i] * 2^(scales[b] - 133), which is always a bf16 number. No
+ * value is off by more than half a step (2^(scales[b] - 134)). A block that holds an
+ * infinity or a NaN gets scale 255 and codes 0 and reads back as NaN throughout.
+ *
+ * gnf4_quantize_act8 writes the checkpoint of x, gnf4_dequantize_act8 reads one back.
+ * x, out device bf16 [rows, K], 16-byte aligned
+ * codes  device int8  [rows, K], 8-byte aligned
+ * scales device uint8 [rows, K/32]
+ * rows >= 0, K % 32 == 0. One kernel launch; rows == 0 launches nothing and accepts NULL
+ * buffers. Outputs may not overlap inputs.
+ * Errors: INVALID_ARG (null/host pointer, rows < 0, K < 1), UNSUPPORTED_SHAPE (K % 32), MISALIGNED.
+ */
+gnf4_status gnf4_quantize_act8(const void* x, int64_t rows, int64_t K, int8_t* codes, uint8_t* scales,
+                               void* stream);
+gnf4_status gnf4_dequantize_act8(const int8_t* codes, const uint8_t* scales, int64_t rows, int64_t K,
+                                 void* out, void* stream);
+
+/*
+ * gnf4_swiglu that also writes the checkpoint of its gate_up rows, in one pass over them:
+ * out is gnf4_swiglu's bit for bit, codes and scales are gnf4_quantize_act8's of gate_up.
+ * gate_up device bf16 [R, 2I], 16-byte aligned; out device bf16 [R, I], 16-byte aligned;
+ * codes device int8 [R, 2I], 8-byte aligned; scales device uint8 [R, 2I/32]. I % 32 == 0.
+ * One kernel launch; R == 0 launches nothing and accepts NULL buffers.
+ */
+gnf4_status gnf4_swiglu_act8(const void* gate_up, int64_t R, int64_t I, void* out, int8_t* codes,
+                             uint8_t* scales, void* stream);
+
+/*
+ * Backward pass of gnf4_swiglu. With sig = 1 / (1 + exp(-gate)) and d = grad_out[r, j]:
+ *   grad_gate_up[r, j]     = bf16_rne( d * up * sig * (1 + gate * (1 - sig)) )
+ *   grad_gate_up[r, I + j] = bf16_rne( d * gate * sig )
+ *   act[r, j]              = what gnf4_swiglu gives for these rows (bit for bit), if act is
+ *                            not NULL: a layer that keeps gate_up, or only its checkpoint,
+ *                            has the down projection's input back from the same pass
+ * The rows are gate_up (bf16), or, with gate_up NULL, the values of the checkpoint codes,
+ * scales. Computed in fp32 (relative error about 2^-17 of |d up sig| (1 + |gate|) and of
+ * |d gate sig| before the rounding; finite gates).
+ * grad_out device bf16 [R, I]; gate_up device bf16 [R, 2I] or NULL; codes device int8 [R, 2I]
+ * (8-byte aligned) and scales device uint8 [R, 2I/32], given exactly if gate_up is not;
+ * grad_gate_up device bf16 [R, 2I]; act device bf16 [R, I] or NULL. bf16 buffers are 16-byte
+ * aligned; outputs may not overlap inputs. I % 8 == 0 (I % 32 == 0 with a checkpoint).
+ * One kernel launch; R == 0 launches nothing and accepts NULL buffers.
+ * Errors: INVALID_ARG, UNSUPPORTED_SHAPE, MISALIGNED.
+ */
+gnf4_status gnf4_swiglu_backward(const void* grad_out, const void* gate_up, const int8_t* codes,
+                                 const uint8_t* scales, int64_t R, int64_t I, void* grad_gate_up,
+                                 void* act, void* stream);
+
+/*
+ * Low-rank adapters beside a projection, all adapters of the call in one launch: each routed
+ * row of the projection (a grouped GEMM call, or one shared projection with E = 1) gets the
+ * product of its own adapter on top. Rows r are sorted by adapter: adapter e owns rows
+ * [adapter_offsets[e], adapter_offsets[e+1]).
+ *   h[r, j]         = sum_k x[tok(r), k] A[e(r), j, k]
+ *   out[dest(r), n] = round16( base[dest(r), n] + scaling[e(r)] w(r) sum_j B[e(r), n, j] h[r, j] )
+ *   tok(r) = row_token ? row_token[r] : r,  w(r) = row_weight ? row_weight[r] : 1,
+ *   dest(r) = row_dest ? row_dest[r] : r,   scaling[e] = 1 if scaling is NULL
+ * Adapters of experts take the arrays of the grouped call itself (and its output as base);
+ * adapters of requests take gnf4_routing_metadata's of the [T, 1] adapter ids, where an id
+ * outside [0, L) is a request without an adapter.
+ * base, out  device, dtype, [T_out, N]; out may be base (in place). Rows that no routed row
+ *            names are not written (with out != base they are not copied either). base may be
+ *            NULL: zeros
+ * x          device, dtype, [T_in, K]
+ * A, B       device, dtype, [L, r, K] and [L, N, r]
+ * dtype      GNF4_DTYPE_BF16 or GNF4_DTYPE_F16, of base, out, x, A and B
+ * adapter_offsets device int64 [L+1]: offsets[0] = 0, non-decreasing, offsets[L] <= R; rows
+ *            at or behind offsets[L] do not exist (their entries are not read)
+ * row_token, row_weight, row_dest as in the grouped call ([R] or NULL; row_dest distinct);
+ *            a row whose token or destination is out of range counts as zeros or is not written
+ * scaling    device fp32 [L], or NULL
+ * h          device fp32 [R, r], or NULL: the rows h, which gnf4_lora_backward wants
+ * L in [1, 2048], r in [8, 128] with r % 8 == 0, K % 8 == 0, N % 8 == 0. 16-bit buffers are
+ * 16-byte aligned, fp32 and int32 ones 4-byte, offsets 8-byte. Sums in fp32; h enters the
+ * second product with about 17 significant bits (two 16-bit terms). Deterministic: the same
+ * call gives the same bits. R == 0 launches nothing and accepts NULL buffers.
+ * flags: 0 or GNF4_CHECK (validates offsets, row arrays and weights on the device first: one
+ * extra kernel and a stream sync).
+ * Errors: INVALID_ARG, UNSUPPORTED_SHAPE, MISALIGNED, DEVICE_STATUS (GNF4_CHECK), CUDA.
+ */
+gnf4_status gnf4_lora_apply(const void* base, const void* x, int dtype, const void* A, const void* B,
+                            const int64_t* adapter_offsets, const int32_t* row_token,
+                            const float* row_weight, const int32_t* row_dest, const float* scaling,
+                            int64_t L, int64_t r, int64_t N, int64_t K, int64_t R, int64_t T_in,
+                            int64_t T_out, void* out, float* h, int flags, void* stream);
+
+/*
+ * Gradients of gnf4_lora_apply (bf16), two launches. With c(r) = scaling[e(r)] w(r) and
+ * src(r) = row_src ? row_src[r] : r (the forward's row_dest):
+ *   grad_h[r, j] = c(r) sum_n grad_out[src(r), n] B[e(r), n, j]
+ *   dx[r, k]     = bf16_rne( dx_base[r, k] + sum_j grad_h[r, j] A[e(r), j, k] )   (routed rows)
+ *   dA[e, j, k]  = sum over e's rows of grad_h[r, j] x[tok(r), k]
+ *   dB[e, n, j]  = sum over e's rows of c(r) grad_out[src(r), n] h[r, j]
+ * dx continues the projection's own input gradient: dx_base is gnf4_dgrad_*'s output (NULL:
+ * zeros), and gnf4_combine_topk sums a token's rows afterwards. dA and dB are written for
+ * every adapter; one without rows gets zeros.
+ * grad_out   device bf16 [T_g, N]
+ * x          device bf16 [T_in, K], or NULL: then x_codes int8 [T_in, K] (8-byte aligned) and
+ *            x_scales uint8 [T_in, K/32] hold its checkpoint (K % 32 == 0)
+ * h          device fp32 [R, r] as the forward wrote it
+ * dx         device bf16 [R, K], may be dx_base; or NULL (with dx_base NULL): not wanted
+ * grad_h     device fp32 [R, r] (written)
+ * dA, dB     device [L, r, K] and [L, N, r] of grad_dtype: GNF4_DTYPE_BF16 or GNF4_DTYPE_F32
+ *            (fp32 sums, rounded once). dA may be NULL, and then x is not given either: a
+ *            layer that has x back only later takes it from gnf4_lora_grad_a
+ * Other arguments, limits and errors as in gnf4_lora_apply. Rows at or behind
+ * adapter_offsets[L] of dx and grad_h are not written. With R == 0 the gradients are written
+ * as zeros (adapter_offsets, dA and dB must then still be given).
+ */
+gnf4_status gnf4_lora_backward(const void* grad_out, const void* x, const int8_t* x_codes,
+                               const uint8_t* x_scales, const float* h, const void* A, const void* B,
+                               const int64_t* adapter_offsets, const int32_t* row_token,
+                               const float* row_weight, const int32_t* row_src, const float* scaling,
+                               int64_t L, int64_t r, int64_t N, int64_t K, int64_t R, int64_t T_in,
+                               int64_t T_g, const void* dx_base, void* dx, float* grad_h, void* dA,
+                               void* dB, int grad_dtype, int flags, void* stream);
+
+/*
+ * gnf4_lora_backward's dA alone, from the grad_h that a call without dA has written: for the
+ * down projection of a layer that keeps its gate_up rows (or their checkpoint), whose input
+ * comes back with gnf4_swiglu_backward, after that call's dx. One launch; arguments, limits
+ * and errors as there.
+ */
+gnf4_status gnf4_lora_grad_a(const float* grad_h, const void* x, const int8_t* x_codes,
+                             const uint8_t* x_scales, const int64_t* adapter_offsets,
+                             const int32_t* row_token, int64_t L, int64_t r, int64_t K, int64_t R,
+                             int64_t T_in, void* dA, int grad_dtype, int flags, void* stream);
+
+/*
  * How many kernels one grouped GEMM call with R routed rows and these flags
  * launches (0 when R == 0; GNF4_CHECK adds one). Host-only, no CUDA call.
  */

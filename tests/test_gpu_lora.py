@@ -1,0 +1,523 @@
+"""Parity of the low-rank adapters and their gradients with the fp64 oracle, through the binding.
+
+Tolerances. u is the output type's half step (bf16 2^-8, fp16 2^-11, fp32 2^-24), relative to
+the value. What comes before that rounding is relative to the oracle's bound (the same sums
+over magnitudes): an fp32 accumulation of n terms is off by at most n 2^-23 of it in any order,
+also when an addition truncates instead of rounding, and every operand that is split into two
+16-bit terms adds 2^-16 (bf16: 2^-9 of the remainder, itself 2^-9; fp16 less), three terms
+2^-24. So with n = K + r (forward), N + r (dx), N + rows (dA), rows (dB), plus 32 for the
+handful of products and joins on the way:
+    |out - want| <= u |want| + (1 + u) (n 2^-23 + 2^-16) bound, and half a step of the type's subnormals
+"""
+import numpy as np
+import pytest
+import torch
+
+from oracle import act8 as A8
+from oracle import glue as GL
+from oracle import gnf4_oracle as O
+from oracle import lora as LO
+
+from gpu_support import build_stack
+
+pytestmark = pytest.mark.gpu
+
+HALF = {torch.bfloat16: 2.0 ** -8, torch.float16: 2.0 ** -11, torch.float32: 2.0 ** -24}
+TINY = {torch.bfloat16: 2.0 ** -134, torch.float16: 2.0 ** -25, torch.float32: 2.0 ** -150}    # half a subnormal step
+
+
+def lib():
+    import bit_grouped_moe_gnf4_b200 as g
+    return g
+
+
+def f64(t):
+    return None if t is None else t.double().cpu().numpy()
+
+
+def near(got, want, bound, n, terms, what):
+    u = HALF[got.dtype]
+    e = n * 2.0 ** -23 + (2.0 ** -16 if terms == 2 else 2.0 ** -24)
+    tol = u * np.abs(want) + (1 + u) * e * bound + TINY[got.dtype]
+    err = np.abs(f64(got) - want)
+    assert np.all(err <= tol), f"{what}: {int((err > tol).sum())} of {err.size} off, worst {float((err / tol).max()):.3g} of the bound"
+
+
+class Problem:
+    """Rows of `counts[e]` per adapter; options as in the call."""
+
+    def __init__(self, counts, r, K, N, dtype=torch.bfloat16, gather=True, scatter=True, weights=True, scaling=True,
+                 spare=0, seed=0, far=0):
+        gen = torch.Generator(device="cuda").manual_seed(seed)
+        rng = np.random.default_rng(seed)
+        L, R = len(counts), int(sum(counts))
+        self.R, self.L, self.spare = R, L, spare
+        off = np.concatenate([[0], np.cumsum(counts)]).astype(np.int64)
+        rand = lambda *s, scale=1.0: (torch.randn(*s, generator=gen, device="cuda") * scale).to(dtype)  # noqa: E731
+        T_in = max(1, R // 2 + 3) if gather else R + spare
+        T_out = R + 5 + far if scatter else R + spare
+        self.x, self.base = rand(T_in, K), rand(T_out, N)
+        self.A, self.B = rand(L, r, K, scale=K ** -0.5), rand(L, N, r, scale=r ** -0.5)
+        self.offsets = torch.from_numpy(off).cuda()
+        # the entries behind the last row are never read: out of range on purpose
+        pad = lambda a: torch.from_numpy(np.concatenate([a, np.full(spare, -7, a.dtype)])).cuda()  # noqa: E731
+        self.tok = pad(rng.integers(0, T_in, R).astype(np.int32)) if gather else None
+        self.dest = pad(rng.permutation(T_out)[:R].astype(np.int32)) if scatter else None
+        self.w = torch.cat([torch.rand(R, generator=gen, device="cuda") + 0.1, torch.full((spare,), float("nan"), device="cuda")]) if weights else None
+        self.s = torch.rand(L, generator=gen, device="cuda") * 2 - 1 if scaling else None
+
+    def rows(self):
+        return dict(row_token=self.tok, row_weight=self.w, scaling=self.s, R=self.R + self.spare)
+
+    def host(self):
+        cut = lambda t: None if t is None else t[:self.R].cpu().numpy()  # noqa: E731
+        return dict(row_token=cut(self.tok), row_weight=cut(self.w), scaling=f64(self.s))
+
+    def forward(self, **kw):
+        g = lib()
+        h = torch.full((self.R + self.spare, self.A.shape[1]), 5.0, device="cuda")
+        out = self.base.clone()
+        g.lora_apply(self.base, self.x, self.A, self.B, self.offsets, row_dest=self.dest, out=out, h=h, **self.rows(), **kw)
+        torch.cuda.synchronize()
+        return out, h
+
+    def check_forward(self):
+        out, h = self.forward()
+        want, wh, bound = LO.lora_apply_f64(f64(self.base), f64(self.x), f64(self.A), f64(self.B),
+                                            self.offsets.cpu().numpy(), row_dest=None if self.dest is None else
+                                            self.dest[:self.R].cpu().numpy(), **self.host())
+        K, r = self.A.shape[2], self.A.shape[1]
+        near(out, want, bound, K + r + 32, 2, "out")
+        hb = np.abs(f64(self.x))[self.host()["row_token"] if self.tok is not None else slice(0, self.R)].max() * \
+            np.abs(f64(self.A)).sum(axis=2).max()
+        near(h[:self.R], wh, np.full_like(wh, hb), K + 32, 3, "h")
+        assert (h[self.R:] == 5).all()
+        free = np.ones(len(out), bool)
+        free[np.arange(self.R) if self.dest is None else self.dest[:self.R].cpu().numpy()] = False
+        assert torch.equal(out[torch.from_numpy(free).cuda()], self.base[torch.from_numpy(free).cuda()])
+        return out, h
+
+    def check_backward(self, grads=torch.bfloat16, act8=False, base=True):
+        g = lib()
+        gen = torch.Generator(device="cuda").manual_seed(99)
+        r, K, N = self.A.shape[1], self.A.shape[2], self.B.shape[1]
+        dy = (torch.randn(self.base.shape, generator=gen, device="cuda") * 0.1).to(torch.bfloat16)
+        Rp = self.R + self.spare
+        h = torch.randn(Rp, r, generator=gen, device="cuda")
+        dxb = torch.randn(Rp, K, generator=gen, device="cuda").to(torch.bfloat16) if base else None
+        x, xv = dict(x=self.x), f64(self.x)
+        if act8:
+            q = g.quantize_act8(self.x)
+            x, xv = dict(act8=q), A8.values_act8(q[0].cpu().numpy(), q[1].cpu().numpy())
+        gh = torch.full((Rp, r), 5.0, device="cuda")
+        dx = torch.full((Rp, K), 3.0, device="cuda").to(torch.bfloat16)
+        out = g.lora_backward(dy, h, self.A, self.B, self.offsets, row_src=self.dest, dx_base=dxb, dx=dx, grad_h=gh,
+                              grad_dtype=grads, **x, **self.rows())
+        torch.cuda.synchronize()
+        assert out[0] is dx and (dx[self.R:] == 3).all() and (gh[self.R:] == 5).all()
+        w = LO.lora_backward_f64(f64(dy), xv, f64(h), f64(self.A), f64(self.B), self.offsets.cpu().numpy(),
+                                 row_src=None if self.dest is None else self.dest[:self.R].cpu().numpy(),
+                                 dx_base=f64(dxb), **self.host())
+        m = int(np.diff(self.offsets.cpu().numpy()).max())
+        terms = 3 if grads == torch.float32 else 2
+        near(gh[:self.R], w["grad_h"], w["grad_h_bound"], N + 32, 3, "grad_h")
+        near(dx[:self.R], w["dx"], w["dx_bound"], N + r + 32, 2, "dx")
+        near(out[1], w["dA"], w["dA_bound"], N + m + 32, terms, "dA")
+        near(out[2], w["dB"], w["dB_bound"], m + 32, terms, "dB")
+        return out
+
+
+ROWS = {
+    "one": [1],
+    "few": [0, 3, 0, 17, 1, 0],
+    "ragged": [33, 0, 64, 100, 16, 15, 1],
+    "long": [700],
+    "skewed": [1500, 0, 2, 1, 40],
+    "many": [i % 3 for i in range(300)],
+    "limit": [1 if i % 17 == 0 else 0 for i in range(2048)],
+}
+
+
+@pytest.mark.parametrize("counts", list(ROWS))
+@pytest.mark.parametrize("r,K,N", [(16, 256, 192), (8, 72, 40), (32, 520, 136)])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+def test_apply_over_row_counts(counts, r, K, N, dtype):
+    Problem(ROWS[counts], r, K, N, dtype=dtype, seed=r).check_forward()
+
+
+@pytest.mark.parametrize("r", [8, 16, 24, 32, 40, 64, 72, 104, 128])
+@pytest.mark.parametrize("K,N", [(8, 8), (2048, 1536), (2888, 5768), (32, 2048)])
+def test_apply_over_sizes(r, K, N):
+    for counts in ([2, 0, 5], [40, 90]):
+        Problem(counts, r, K, N, dtype=torch.float16 if r % 16 else torch.bfloat16, seed=K).check_forward()
+
+
+@pytest.mark.parametrize("kw", [dict(gather=False), dict(scatter=False), dict(weights=False), dict(scaling=False),
+                                dict(gather=False, scatter=False, weights=False, scaling=False), dict(spare=9),
+                                dict(spare=40, gather=False, scatter=False)])
+def test_apply_without_each_array(kw):
+    for counts in ([3, 0, 20], [60, 1]):
+        Problem(counts, 16, 264, 200, **kw).check_forward()
+
+
+@pytest.mark.parametrize("counts", list(ROWS))
+@pytest.mark.parametrize("r,K,N", [(16, 256, 192), (8, 96, 40), (40, 544, 136)])
+@pytest.mark.parametrize("grads", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("act8", [False, True])
+def test_backward_over_row_counts(counts, r, K, N, grads, act8):
+    Problem(ROWS[counts], r, K, N, seed=r).check_backward(grads, act8)
+
+
+@pytest.mark.parametrize("r", [8, 24, 32, 64, 72, 128])
+@pytest.mark.parametrize("K,N", [(8, 8), (32, 8), (2048, 1536), (1032, 2888)])
+def test_backward_over_sizes(r, K, N):
+    for counts, grads in (([2, 0, 5], torch.float32), ([40, 300], torch.bfloat16)):
+        Problem(counts, r, K, N, seed=K).check_backward(grads, act8=K % 32 == 0)
+
+
+@pytest.mark.parametrize("kw", [dict(gather=False), dict(scatter=False), dict(weights=False), dict(scaling=False),
+                                dict(gather=False, scatter=False, weights=False, scaling=False), dict(spare=9),
+                                dict(spare=40, gather=False, scatter=False)])
+def test_backward_without_each_array(kw):
+    for counts in ([3, 0, 20], [60, 1]):
+        Problem(counts, 16, 264, 200, **kw).check_backward()
+        Problem(counts, 16, 264, 200, **kw).check_backward(base=False)
+
+
+def test_long_segments_split_over_a_cluster():
+    # enough rows of one adapter for every cluster size of the gradient sums
+    for m in (1100, 2300, 5000, 9001):
+        Problem([m], 16, 136, 72, seed=m).check_backward(torch.float32)
+
+
+def test_in_place_and_deterministic():
+    p = Problem([7, 0, 50, 1], 16, 256, 320)
+    out, _ = p.forward()
+    y = p.base.clone()
+    assert lib().lora_apply(y, p.x, p.A, p.B, p.offsets, row_dest=p.dest, **p.rows()) is y
+    assert torch.equal(y, out)
+    assert torch.equal(p.forward()[0], out)
+    a, b = p.check_backward(), p.check_backward()
+    assert all(torch.equal(u, v) for u, v in zip(a, b))
+    # dx continues dx_base in place
+    g = lib()
+    dy, h = torch.randn_like(p.base), torch.randn(p.R, 16, device="cuda")
+    dxb = torch.randn(p.R, 256, device="cuda").to(torch.bfloat16)
+    kw = dict(x=p.x, row_src=p.dest, **p.rows())
+    want = g.lora_backward(dy, h, p.A, p.B, p.offsets, dx_base=dxb, **kw)[0]
+    got = g.lora_backward(dy, h, p.A, p.B, p.offsets, dx_base=dxb, dx=dxb, **kw)[0]
+    assert got is dxb and torch.equal(got, want)
+
+
+def test_base_none_is_zeros():
+    g = lib()
+    p = Problem([5, 40], 16, 128, 64, scatter=False)
+    out = torch.full_like(p.base, 9.0)
+    g.lora_apply(None, p.x, p.A, p.B, p.offsets, out=out, **p.rows())
+    want = g.lora_apply(torch.zeros_like(p.base), p.x, p.A, p.B, p.offsets, out=p.base.clone(), **p.rows())
+    assert torch.equal(out, want)
+
+
+def test_parts_of_the_backward():
+    g = lib()
+    p = Problem([30, 0, 3], 24, 160, 72)
+    dy, h = torch.randn_like(p.base), torch.randn(p.R, 24, device="cuda")
+    kw = dict(row_src=p.dest, **p.rows())
+    dx, dA, dB = g.lora_backward(dy, h, p.A, p.B, p.offsets, x=p.x, **kw)
+    gh = torch.empty(p.R, 24, device="cuda")
+    dx2, none, dB2 = g.lora_backward(dy, h, p.A, p.B, p.offsets, grad_h=gh, **kw)
+    assert none is None and torch.equal(dx2, dx) and torch.equal(dB2, dB)
+    assert torch.equal(g.lora_grad_a(gh, p.offsets, x=p.x, row_token=p.tok), dA)
+    q = g.quantize_act8(p.x)
+    want = g.lora_backward(dy, h, p.A, p.B, p.offsets, act8=q, **kw)
+    assert torch.equal(g.lora_grad_a(gh, p.offsets, act8=q, row_token=p.tok), want[1])
+    none, dA3, dB3 = g.lora_backward(dy, h, p.A, p.B, p.offsets, x=p.x, want_dx=False, **kw)
+    assert none is None and torch.equal(dA3, dA) and torch.equal(dB3, dB)
+
+
+def test_no_rows():
+    g = lib()
+    p = Problem([0, 0, 0], 16, 64, 32)
+    out = p.base.clone()
+    g.lora_apply(p.base, p.x, p.A, p.B, p.offsets, row_dest=p.dest, out=out, **p.rows())
+    assert torch.equal(out, p.base)
+    h = torch.empty(0, 16, device="cuda")
+    for dt in (torch.bfloat16, torch.float32):
+        dx, dA, dB = g.lora_backward(p.base, h, p.A, p.B, p.offsets, x=p.x, grad_dtype=dt, row_src=p.dest, **p.rows())
+        assert dx.shape == (0, 64) and not dA.any() and not dB.any() and dA.dtype == dt
+    # an upper bound with no row behind it
+    p = Problem([0, 0, 0], 16, 64, 32, spare=20)
+    out, hh = p.forward()
+    assert torch.equal(out, p.base) and (hh == 5).all()
+    p.check_backward()
+
+
+def test_a_row_that_is_not_finite_stays_alone():
+    for bad in (float("inf"), float("nan")):
+        p = Problem([40, 3], 24, 128, 64, gather=False, scatter=False)
+        clean, _ = p.forward()
+        p.x[17, 5] = bad
+        out, _ = p.forward()
+        keep = torch.arange(43, device="cuda") != 17
+        assert torch.equal(out[keep], clean[keep]) and not torch.isfinite(out[17]).any()
+    # tokens that no row names, and adapters without rows, may hold anything
+    p = Problem([3, 0, 4], 16, 64, 64)
+    clean, _ = p.forward()
+    named = torch.zeros(len(p.x), dtype=torch.bool, device="cuda")
+    named[p.tok.long()] = True
+    p.x[~named] = float("nan")
+    p.A[1] = float("nan")
+    p.B[1] = float("inf")
+    assert torch.equal(p.forward()[0], clean)
+
+
+def test_an_infinite_product_is_infinite():
+    # h overflows to infinity in one rank: B's sign decides, nothing turns into NaN
+    g = lib()
+    x = torch.full((1, 64), 3e38, device="cuda").to(torch.bfloat16)
+    A, B = torch.zeros(1, 16, 64, device="cuda"), torch.zeros(1, 8, 16, device="cuda")
+    A[0, 0] = 2.0
+    B[0, :, 0] = torch.tensor([1.0, -1.0] * 4)
+    off = torch.tensor([0, 1], device="cuda")
+    out = g.lora_apply(torch.zeros(1, 8, device="cuda").to(torch.bfloat16), x, A.bfloat16(), B.bfloat16(), off)
+    assert out[0].tolist() == [float("inf"), float("-inf")] * 4
+
+
+def test_fp16_product_past_the_types_range():
+    # h = 256 * 300 does not fit in fp16; the output does
+    x = torch.full((3, 256), 300.0, device="cuda").half()
+    A = torch.ones(1, 8, 256, device="cuda").half()
+    B = torch.full((1, 16, 8), 2.0 ** -6, device="cuda").half()
+    off = torch.tensor([0, 3], device="cuda")
+    out = lib().lora_apply(torch.zeros(3, 16, device="cuda").half(), x, A, B, off)
+    assert (out == 9600.0).all()                        # 8 * 76800 / 64
+
+
+def test_row_indices_out_of_range_are_left_out():
+    p = Problem([6, 5], 16, 64, 48)
+    ok, _ = p.forward()
+    tok, dest = p.tok.clone(), p.dest.clone()
+    p.tok[2], p.dest[7] = len(p.x), -1
+    out, _ = p.forward()
+    want = ok.clone()
+    want[dest[7].long()] = p.base[dest[7].long()]
+    want[dest[2].long()] = p.base[dest[2].long()]       # zeros on top
+    assert torch.equal(out, want)
+
+
+@pytest.mark.parametrize("what", ["decrease", "past", "first", "token", "dest", "weight"])
+def test_checked_calls_refuse_bad_rows(what):
+    g = lib()
+    p = Problem([4, 3, 5], 16, 64, 48)
+    if what == "decrease":
+        p.offsets[1] = 9
+    elif what == "past":
+        p.offsets[3] = 13
+    elif what == "first":
+        p.offsets[0] = 1
+    elif what == "token":
+        p.tok[11] = len(p.x)
+    elif what == "dest":
+        p.dest[0] = -1
+    else:
+        p.w[3] = float("inf")
+    out = p.base.clone()
+    with pytest.raises(g.Gnf4Error) as e:
+        g.lora_apply(p.base, p.x, p.A, p.B, p.offsets, row_dest=p.dest, out=out, flags=g.GNF4_CHECK, **p.rows())
+    assert e.value.status == 5
+    h = torch.zeros(12, 16, device="cuda")
+    with pytest.raises(g.Gnf4Error):
+        g.lora_backward(p.base, h, p.A, p.B, p.offsets, x=p.x, row_src=p.dest, flags=g.GNF4_CHECK, **p.rows())
+    torch.cuda.synchronize()
+    assert torch.equal(out, p.base)
+
+
+def test_checked_calls_pass_good_rows():
+    p = Problem([4, 0, 5], 16, 64, 48, spare=3)
+    a, b = p.forward()[0], p.forward(flags=lib().GNF4_CHECK)[0]
+    assert torch.equal(a, b)
+
+
+def test_far_rows_and_adapters():
+    # element offsets past 2^31 in base, out, A and dA
+    g = lib()
+    p = Problem([2, 3], 16, 64, 2048, far=1_050_000)
+    p.dest[:5] = torch.tensor([1_050_000, 1_050_006, 3, 1_049_999, 1_050_009], dtype=torch.int32, device="cuda")
+    rows = p.dest.long()
+    near_base = p.base[rows].clone()
+    small = g.lora_apply(near_base, p.x, p.A, p.B, p.offsets, **p.rows())
+    y = g.lora_apply(p.base, p.x, p.A, p.B, p.offsets, row_dest=p.dest, **p.rows())
+    assert torch.equal(y[rows], small)
+    del p, y
+    L, r, K = 2048, 128, 8200
+    A = torch.zeros(L, r, K, dtype=torch.bfloat16, device="cuda")
+    B = torch.zeros(L, 8, r, dtype=torch.bfloat16, device="cuda")
+    gen = torch.Generator(device="cuda").manual_seed(1)
+    A[-1] = torch.randn(r, K, generator=gen, device="cuda") * K ** -0.5
+    B[-1] = torch.randn(8, r, generator=gen, device="cuda")
+    x = torch.randn(3, K, generator=gen, device="cuda").to(torch.bfloat16)
+    off = torch.zeros(L + 1, dtype=torch.int64, device="cuda")
+    off[-1] = 3
+    base = torch.zeros(3, 8, dtype=torch.bfloat16, device="cuda")
+    h = torch.empty(3, r, device="cuda")
+    out = g.lora_apply(base.clone(), x, A, B, off, h=h)
+    off1 = torch.tensor([0, 3], device="cuda")
+    assert torch.equal(out, g.lora_apply(base.clone(), x, A[-1:].contiguous(), B[-1:].contiguous(), off1))
+    dy = torch.randn(3, 8, generator=gen, device="cuda").to(torch.bfloat16)
+    dx, dA, dB = g.lora_backward(dy, h, A, B, off, x=x)
+    dx1, dA1, dB1 = g.lora_backward(dy, h, A[-1:].contiguous(), B[-1:].contiguous(), off1, x=x)
+    assert torch.equal(dx, dx1) and torch.equal(dA[-1:], dA1) and torch.equal(dB[-1:], dB1)
+    assert not dA[:-1].any() and not dB[:-1].any()
+
+
+def test_captured_calls_replay_and_share_nothing():
+    g = lib()
+    probs = [Problem([9, 0, 30], 16, 128, 96, seed=i) for i in range(2)]
+    graphs, outs = [], []
+    for p in probs:
+        p.dy, p.h = torch.randn_like(p.base), torch.randn(p.R, 16, device="cuda")
+
+        def step(p=p):
+            y = g.lora_apply(p.base, p.x, p.A, p.B, p.offsets, row_dest=p.dest, out=p.base.clone(), **p.rows())
+            return (y, *g.lora_backward(p.dy, p.h, p.A, p.B, p.offsets, x=p.x, row_src=p.dest, **p.rows()))
+
+        p.step = step
+        step()
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            outs.append(step())
+        graphs.append(graph)
+    streams = [torch.cuda.Stream() for _ in probs]
+    for turn in range(3):
+        for p in probs:
+            p.x.copy_(torch.randn_like(p.x))
+            p.dy.copy_(torch.randn_like(p.dy))
+        torch.cuda.synchronize()
+        for graph, s in zip(graphs, streams):             # both at once
+            with torch.cuda.stream(s):
+                graph.replay()
+        torch.cuda.synchronize()
+        for p, out in zip(probs, outs):
+            assert all(torch.equal(a, b) for a, b in zip(out, p.step()))
+
+
+def test_other_stream():
+    g = lib()
+    p = Problem([9, 0, 300], 32, 512, 640)
+    want, h = p.forward()
+    s = torch.cuda.Stream()
+    out = p.base.clone()
+    gh = torch.empty(p.R, 32, device="cuda")
+    torch.cuda.synchronize()
+    g.lora_apply(p.base, p.x, p.A, p.B, p.offsets, row_dest=p.dest, out=out, stream=s, **p.rows())
+    got = g.lora_backward(p.base, h, p.A, p.B, p.offsets, x=p.x, row_src=p.dest, grad_h=gh, stream=s, **p.rows())
+    s.synchronize()
+    ref = g.lora_backward(p.base, h, p.A, p.B, p.offsets, x=p.x, row_src=p.dest, **p.rows())
+    torch.cuda.synchronize()
+    assert torch.equal(out, want) and all(torch.equal(a, b) for a, b in zip(got, ref))
+
+
+def test_requests_through_routing_metadata():
+    """Adapter ids of a batch of tokens, some without one, on top of one shared 4-bit projection."""
+    g = lib()
+    T, K, N, L, r = 37, 256, 128, 5, 16
+    Wd, Sd, Wh, Sh = build_stack("nf4", 1, N, K)
+    gen = torch.Generator(device="cuda").manual_seed(3)
+    x = torch.randn(T, K, generator=gen, device="cuda").to(torch.bfloat16)
+    A = (torch.randn(L, r, K, generator=gen, device="cuda") / 16).to(torch.bfloat16)
+    B = torch.randn(L, N, r, generator=gen, device="cuda").to(torch.bfloat16)
+    ids = torch.randint(-1, L, (T, 1), generator=gen, device="cuda", dtype=torch.int32)
+    y = g.grouped_gemm("nf4", x, Wd, Sd, torch.tensor([0, T], device="cuda"), R=T)
+    base = y.clone()
+    off, tok, _, dst = g.routing_metadata(ids, None, L)
+    g.lora_apply(y, x, A, B, off, row_token=tok, row_dest=dst, R=T)
+    torch.cuda.synchronize()
+    want, bound = f64(base), np.zeros((T, N))
+    for i, e in enumerate(ids[:, 0].tolist()):
+        if e >= 0:
+            h = f64(A[e]) @ f64(x[i])
+            want[i] += f64(B[e]) @ h
+            bound[i] = (np.abs(f64(A[e])) @ np.abs(f64(x[i]))).max() * np.abs(f64(B[e])).sum(axis=1)
+    near(y, want, bound, K + r + 32, 2, "y")
+    gone = ids[:, 0] < 0
+    assert gone.any() and torch.equal(y[gone], base[gone])
+
+
+def test_expert_layer_trains_its_adapters():
+    """One MoE layer, forward and backward, as a trainer runs it: routing, gate_up with adapters,
+    SwiGLU with an 8-bit checkpoint, down with adapters, combine; then the gradients of both
+    pairs of adapters and of the tokens, against the oracles' chain on the same rounded values."""
+    from oracle import dgrad as D
+    g = lib()
+    T, k, E, H, I, r = 45, 2, 6, 192, 128, 16
+    Wd, Sd, Wh, Sh = build_stack("nf4", E, 2 * I, H, seed=1)
+    Vd, Ud, Vh, Uh = build_stack("mxfp4", E, H, I, seed=2)
+    gen = torch.Generator(device="cuda").manual_seed(5)
+    rand = lambda *s, scale=1.0: (torch.randn(*s, generator=gen, device="cuda") * scale).to(torch.bfloat16)  # noqa: E731
+    x, dout = rand(T, H), rand(T, H)
+    A1, B1, A2, B2 = rand(E, r, H, scale=0.1), rand(E, 2 * I, r, scale=0.05), rand(E, r, I, scale=0.1), rand(E, H, r, scale=0.05)
+    s1, s2 = torch.rand(E, generator=gen, device="cuda") + 0.5, torch.rand(E, generator=gen, device="cuda") + 0.5
+    ids = torch.stack([torch.randperm(E, generator=gen, device="cuda")[:k] for _ in range(T)]).to(torch.int32)
+    wts = torch.rand(T, k, generator=gen, device="cuda")
+    R = T * k
+
+    # forward
+    off, tok, w, dst = g.routing_metadata(ids, wts, E)
+    h1, h2 = torch.empty(R, r, device="cuda"), torch.empty(R, r, device="cuda")
+    gu0 = g.grouped_gemm("nf4", x, Wd, Sd, off, row_token=tok)
+    gu = g.lora_apply(gu0, x, A1, B1, off, row_token=tok, scaling=s1, h=h1, out=gu0.clone())
+    act, codes, scales = g.swiglu_act8(gu)
+    y0 = g.grouped_gemm("mxfp4", act, Vd, Ud, off, row_weight=w, row_dest=dst, T_out=R)
+    y = g.lora_apply(y0, act, A2, B2, off, row_weight=w, row_dest=dst, scaling=s2, h=h2, out=y0.clone())
+    out = g.combine_topk(y, T, k)
+    # backward: a token's slots all get its gradient, so rows read it through their token
+    d_act0 = g.dgrad("mxfp4", dout, Vd, Ud, off, row_src=tok, row_weight=w)
+    gh2 = torch.empty(R, r, device="cuda")
+    d_act, _, dB2 = g.lora_backward(dout, h2, A2, B2, off, row_src=tok, row_weight=w, scaling=s2, dx_base=d_act0,
+                                    dx=torch.empty_like(d_act0), grad_h=gh2)
+    d_gu, act_again = g.swiglu_backward(d_act, act8=(codes, scales), rebuild=True)
+    dA2 = g.lora_grad_a(gh2, off, x=act_again)
+    dx0 = g.dgrad("nf4", d_gu, Wd, Sd, off, R=R)
+    xq = g.quantize_act8(x)
+    dx, dA1, dB1 = g.lora_backward(d_gu, h1, A1, B1, off, act8=xq, row_token=tok, scaling=s1, dx_base=dx0,
+                                   dx=torch.empty_like(dx0))
+    slot_row = torch.empty(R, dtype=torch.int32, device="cuda")
+    slot_row[dst.long()] = torch.arange(R, dtype=torch.int32, device="cuda")
+    d_x = g.combine_topk(dx, T, k, row_of_slot=slot_row)
+    g.device_status()
+
+    o, tk, ds, ww = (v.cpu().numpy() for v in (off, tok, dst, w))
+    want, wh, b = LO.lora_apply_f64(f64(gu0), f64(x), f64(A1), f64(B1), o, row_token=tk, scaling=f64(s1))
+    near(gu, want, b, H + r + 32, 2, "gate_up")
+    want, _, b = LO.lora_apply_f64(f64(y0), f64(act), f64(A2), f64(B2), o, row_weight=ww, row_dest=ds, scaling=f64(s2))
+    near(y, want, b, I + r + 32, 2, "down")
+    xb, gb = x.view(torch.int16).cpu().numpy().view(np.uint16), dout.view(torch.int16).cpu().numpy().view(np.uint16)
+    # against the exact layer the rounded intermediate rows leave a few bf16 steps of each row's largest value
+    exact_gu = O.grouped_rows_f64("nf4", xb, Wh, Sh, o, tk, None, H, np.arange(R))
+    exact_gu, _, _ = LO.lora_apply_f64(exact_gu, f64(x), f64(A1), f64(B1), o, row_token=tk, scaling=f64(s1))
+    assert np.all(np.abs(f64(gu) - exact_gu).max(axis=1) <= 2e-2 * np.abs(exact_gu).max(axis=1))
+    bw = LO.lora_backward_f64(f64(dout), f64(act_again), f64(h2), f64(A2), f64(B2), o, row_src=tk, row_weight=ww,
+                              scaling=f64(s2), dx_base=f64(d_act0))
+    m = int(np.diff(o).max())
+    near(d_act, bw["dx"], bw["dx_bound"], H + r + 32, 2, "d_act")
+    near(dA2, bw["dA"], bw["dA_bound"], H + m + 32, 2, "dA of down")
+    near(dB2, bw["dB"], bw["dB_bound"], m + 32, 2, "dB of down")
+    gu8 = A8.values_act8(codes.cpu().numpy(), scales.cpu().numpy())
+    sw = A8.swiglu_backward_f64(f64(d_act), gu8)
+    assert np.all(np.abs(f64(d_gu) - sw) <= 2.0 ** -8 * np.abs(sw) + 2.0 ** -15 * A8.swiglu_backward_bound(f64(d_act), gu8) + 2.0 ** -126)
+    want = GL.swiglu_rows_f64(O.bf16_bits(gu8))
+    assert np.all(np.abs(f64(act_again) - want) <= (2.0 ** -8 + 2.0 ** -16) * np.abs(want) + 2.0 ** -118)
+    bw = LO.lora_backward_f64(f64(d_gu), A8.values_act8(xq[0].cpu().numpy(), xq[1].cpu().numpy()), f64(h1), f64(A1),
+                              f64(B1), o, row_token=tk, scaling=f64(s1), dx_base=f64(dx0))
+    near(dx, bw["dx"], bw["dx_bound"], 2 * I + r + 32, 2, "dx")
+    near(dA1, bw["dA"], bw["dA_bound"], 2 * I + m + 32, 2, "dA of gate_up")
+    near(dB1, bw["dB"], bw["dB_bound"], m + 32, 2, "dB of gate_up")
+    ref = D.dgrad_rows_f64("mxfp4", gb, Vh, Uh, o, tk, ww, np.arange(R))
+    assert np.all(np.abs(f64(d_act0) - ref).max(axis=1) <= 2e-2 * np.abs(ref).max(axis=1))
+    sums = np.zeros((T, H))
+    np.add.at(sums, tk, f64(dx))
+    top = np.zeros((T, H))
+    np.add.at(top, tk, np.abs(f64(dx)))
+    assert np.all(np.abs(f64(d_x) - sums) <= 2.0 ** -8 * np.abs(sums) + 2.0 ** -21 * top)
+    assert torch.isfinite(out).all()
