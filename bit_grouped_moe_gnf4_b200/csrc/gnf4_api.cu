@@ -385,8 +385,8 @@ static gnf4_status check_device(std::initializer_list<const void*> ptrs) {
 
 static gnf4_status check_act8_args(const void* x16, const void* codes, const void* scales) {
     if (!x16 || !codes || !scales) return fail(GNF4_ERR_INVALID_ARG, "null pointer argument");
-    if (!aligned16(x16) || !aligned8(codes))
-        return fail(GNF4_ERR_MISALIGNED, "bf16 rows must be 16-byte and codes 8-byte aligned");
+    if (!aligned16(x16) || !aligned16(codes))
+        return fail(GNF4_ERR_MISALIGNED, "bf16 rows and codes must be 16-byte aligned");
     return check_device({x16, codes, scales});
 }
 
@@ -422,8 +422,8 @@ static gnf4_status check_lora_sizes(const LoraCommon& c) {
     if (c.r % 8 || c.r > 128) return fail(GNF4_ERR_UNSUPPORTED_SHAPE, "the rank must be a multiple of 8 up to 128");
     if (c.K % 8 || c.N % 8) return fail(GNF4_ERR_UNSUPPORTED_SHAPE, "K and N must be multiples of 8");
     if (c.L > 2048) return fail(GNF4_ERR_UNSUPPORTED_SHAPE, "at most 2048 adapters");
-    if (c.K > (1 << 24) || c.N > (1 << 24) || c.R > INT_MAX || c.n_a > INT_MAX || c.n_b > INT_MAX)
-        return fail(GNF4_ERR_UNSUPPORTED_SHAPE, "K and N must be at most 2^24, row counts must fit in int32");
+    if (c.K > (1 << 24) || c.N > (1 << 24) || c.R > (1 << 30) || c.n_a > INT_MAX || c.n_b > INT_MAX)
+        return fail(GNF4_ERR_UNSUPPORTED_SHAPE, "K and N must be at most 2^24, R at most 2^30, row counts must fit in int32");
     if (!c.row_a && c.n_a < c.R) return fail(GNF4_ERR_INVALID_ARG, "row_token is NULL but T_in < R");
     if (!c.row_b && c.n_b < c.R) return fail(GNF4_ERR_INVALID_ARG, "the destination rows are NULL but there are fewer than R");
     return GNF4_OK;
@@ -706,8 +706,8 @@ gnf4_status gnf4_swiglu_backward(const void* grad_out, const void* gate_up, cons
     if (!grad_out || !grad_gate_up) return fail(GNF4_ERR_INVALID_ARG, "null pointer argument");
     if (gate_up ? (codes || scales) : !(codes && scales))
         return fail(GNF4_ERR_INVALID_ARG, "give either gate_up or its checkpoint (codes and scales)");
-    if (!aligned16(grad_out) || !aligned16(gate_up) || !aligned16(grad_gate_up) || !aligned16(act) || !aligned8(codes))
-        return fail(GNF4_ERR_MISALIGNED, "bf16 rows must be 16-byte and codes 8-byte aligned");
+    if (!aligned16(grad_out) || !aligned16(gate_up) || !aligned16(grad_gate_up) || !aligned16(act) || !aligned16(codes))
+        return fail(GNF4_ERR_MISALIGNED, "bf16 rows and codes must be 16-byte aligned");
     if ((st = check_device({grad_out, gate_up, codes, scales, grad_gate_up, act})) != GNF4_OK) return st;
     cudaError_t e = launch_swiglu_backward(grad_out, gate_up, codes, scales, R, I, grad_gate_up, act,
                                            reinterpret_cast<cudaStream_t>(stream));
@@ -725,8 +725,8 @@ gnf4_status gnf4_lora_apply(const void* base, const void* x, int dtype, const vo
     if (st != GNF4_OK || R == 0) return st;
     if ((st = check_lora_buffers(c)) != GNF4_OK) return st;
     if (!x || !out) return fail(GNF4_ERR_INVALID_ARG, "null pointer argument");
-    if (!aligned16(x) || !aligned16(base) || !aligned16(out) || !aligned4(h))
-        return fail(GNF4_ERR_MISALIGNED, "x, base and out must be 16-byte and h 4-byte aligned");
+    if (!aligned16(x) || !aligned16(base) || !aligned16(out) || !aligned16(h))
+        return fail(GNF4_ERR_MISALIGNED, "x, base, out and h must be 16-byte aligned");
     if ((st = check_lora_device(c)) != GNF4_OK || (st = check_device({x, base, out, h})) != GNF4_OK) return st;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     if ((flags & GNF4_CHECK) && (st = check_lora_rows(c, s)) != GNF4_OK) return st;
@@ -773,9 +773,9 @@ gnf4_status gnf4_lora_backward(const void* grad_out, const void* x, const int8_t
     } else if (!adapter_offsets || !aligned8(adapter_offsets)) {
         return fail(GNF4_ERR_INVALID_ARG, "adapter_offsets must be given, 8-byte aligned");
     }
-    if (!aligned16(grad_out) || !aligned16(x) || !aligned8(x_codes) || !aligned16(dx_base) || !aligned16(dx) ||
-        !aligned4(h) || !aligned4(grad_h) || !aligned16(dA) || !aligned16(dB))
-        return fail(GNF4_ERR_MISALIGNED, "16-bit rows, dA and dB must be 16-byte, x_codes 8-byte, h and grad_h 4-byte aligned");
+    if (!aligned16(grad_out) || !aligned16(x) || !aligned16(x_codes) || !aligned16(dx_base) || !aligned16(dx) ||
+        !aligned16(h) || !aligned16(grad_h) || !aligned16(dA) || !aligned16(dB))
+        return fail(GNF4_ERR_MISALIGNED, "16-bit rows, x_codes, h, grad_h, dA and dB must be 16-byte aligned");
     if ((st = check_lora_device(c)) != GNF4_OK) return st;
     if ((st = check_device({grad_out, x, x_codes, x_scales, h, dx_base, dx, grad_h, dA, dB})) != GNF4_OK) return st;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
@@ -837,9 +837,9 @@ gnf4_status gnf4_lora_grad_a(const float* grad_h, const void* x, const int8_t* x
     if (x_codes && K % 32) return fail(GNF4_ERR_UNSUPPORTED_SHAPE, "a checkpoint of x needs K % 32 == 0");
     if (!dA || !adapter_offsets || (R > 0 && !grad_h)) return fail(GNF4_ERR_INVALID_ARG, "null pointer argument");
     if (R > 0 && (st = check_lora_x(x, x_codes, x_scales, false)) != GNF4_OK) return st;
-    if (!aligned16(x) || !aligned8(x_codes) || !aligned4(grad_h) || !aligned16(dA) || !aligned8(adapter_offsets) ||
+    if (!aligned16(x) || !aligned16(x_codes) || !aligned16(grad_h) || !aligned16(dA) || !aligned8(adapter_offsets) ||
         !aligned4(row_token))
-        return fail(GNF4_ERR_MISALIGNED, "x and dA must be 16-byte, x_codes and adapter_offsets 8-byte, grad_h and row_token 4-byte aligned");
+        return fail(GNF4_ERR_MISALIGNED, "x, x_codes, grad_h and dA must be 16-byte, adapter_offsets 8-byte and row_token 4-byte aligned");
     if ((st = check_device({grad_h, x, x_codes, x_scales, adapter_offsets, row_token, dA})) != GNF4_OK) return st;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     if (R > 0 && (flags & GNF4_CHECK) && (st = check_lora_rows(c, s)) != GNF4_OK) return st;

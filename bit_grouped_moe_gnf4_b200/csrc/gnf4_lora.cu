@@ -16,8 +16,7 @@
 // distributed shared memory when the cluster has more than one CTA), and then the warps
 // split the output columns of the second. x, base and out are touched once.
 //
-// lora_grads_kernel sums over an adapter's rows: a warp owns a slab of the gradient's
-// columns, rows are the MMA's contraction index.
+// lora_grads_kernel sums over an adapter's rows (below).
 //
 // Rounding: sums are fp32. h (and g) enter the second product as two 16-bit terms (value
 // and remainder: about 17 significant bits, so that what the caller sees is the one
@@ -557,34 +556,143 @@ cudaError_t launch_rows_r(const LoraRowsArgs& a, bool bwd, bool f16, cudaStream_
 // ---------------------------------------------------------------------------
 // gradients of the adapters
 // ---------------------------------------------------------------------------
-template <int RP>
+// One gradient of one adapter: sum over its rows of left[r, j] right[row r, n], rows the MMA's
+// contraction index. A CTA owns WC * SC columns (SC a warp) and walks the adapter's rows in
+// stages of 32 WR: the rows of `right` are gathered into shared memory by 16-byte asynchronous
+// copies, three stages deep (the gather's latency, index then row, is what a warp alone cannot
+// hide), while `left` is read ahead by a stage into registers and split into its 16-bit terms
+// once for all warps. Both fragments come out of shared memory transposed.
+constexpr int kGradStages = 3;
+
+template <int RP, int WR, int TERMS>
 struct GradShape {
-    static constexpr int CT = RP <= 32 ? 8 : 4;      // MMA column tiles of a warp's slab
-    static constexpr int SC = 8 * CT;                // its columns
+    static constexpr int CT = RP <= 32 ? 8 : 4;          // MMA column tiles of a warp's slab
+    static constexpr int SC = 8 * CT;                    // its columns
     static constexpr int MT = RP / 16;
-    static constexpr int kStride = SC + 4;           // floats of a row of the sum in shared memory
+    static constexpr int WC = kLoraWarps / WR;
+    static constexpr int CW = WC * SC;                   // columns of the CTA
+    static constexpr int SR = 32 * WR;                   // rows of a stage
+    static constexpr int kPitch16 = 2 * CW + 16;         // bytes a row in shared memory: bf16,
+    static constexpr int kPitch8 = CW + 16;              // codes; conflict-free fragment loads
+    static constexpr int kPlane = RP + 8;                // elements a row of a term plane
+    static constexpr int kStride = SC + 4;               // floats of a row of the sum
+    static constexpr int kLeft = (SR * RP / 4 + kLoraThreads - 1) / kLoraThreads;   // float4 of left a thread and stage
+    static constexpr size_t stage_bytes = (size_t)SR * kPitch16;
+    static constexpr size_t plane_bytes = (size_t)TERMS * SR * kPlane * 2;          // one of two buffers
+    static constexpr size_t scale_bytes = (size_t)SR * (CW / 32);                   // one of two buffers
+    static constexpr size_t work = kGradStages * stage_bytes + 2 * plane_bytes + 2 * scale_bytes + 2 * SR * 4;
+    static constexpr size_t sums = sizeof(float) * (size_t)kLoraWarps * RP * kStride;
+    static constexpr size_t smem = work > sums ? work : sums;
 };
 
-template <int RP>
-constexpr size_t grads_smem() {
-    return sizeof(float) * (size_t)kLoraWarps * RP * GradShape<RP>::kStride;
+__device__ __forceinline__ void copy_async16(uint32_t dst, const void* src, uint32_t bytes) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copy_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+
+__device__ __forceinline__ void ldmatrix4_trans(uint32_t (&d)[4], uint32_t addr) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(d[0]), "=r"(d[1]), "=r"(d[2]), "=r"(d[3]) : "r"(addr) : "memory");
 }
 
-// One gradient of one adapter, `left` [R, r] fp32 (times the row's factor) against the rows
-// of `right` [*, C]: sum_r left[r, j] right[row r, n]. CTA: WC = 8 / WR slabs of columns, the
-// adapter's rows dealt out 16 at a time to WR warps of each of the cluster's CTAs.
 template <int RP, int WR, int TERMS, bool Q8>
-__device__ __forceinline__ void grad_body(const LoraGradArgs& p, const LoraGradSide& d, int e, int slab0, float* s_red) {
-    using S = GradShape<RP>;
-    constexpr int CT = S::CT, MT = S::MT, WC = kLoraWarps / WR;
+__device__ __forceinline__ void grad_body(const LoraGradArgs& p, const LoraGradSide& d, int e, int col0, uint8_t* smem) {
+    using S = GradShape<RP, WR, TERMS>;
+    constexpr int CT = S::CT, MT = S::MT, WC = S::WC, CW = S::CW, SR = S::SR;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int g = lane >> 2, t = lane & 3;
     const int wc = warp % WC, wr = warp / WC;
     const int CS = (int)cluster_size(), crank = (int)cluster_rank();
-    const int col = (slab0 + wc) * S::SC + CT * g;       // first of this lane's CT columns of every row
-    const bool in = col < d.C;
+    uint8_t* s_stage = smem;
+    uint16_t* s_plane = reinterpret_cast<uint16_t*>(smem + kGradStages * S::stage_bytes);
+    uint8_t* s_scale = smem + kGradStages * S::stage_bytes + 2 * S::plane_bytes;
+    int* s_row = reinterpret_cast<int*>(s_scale + 2 * S::scale_bytes);
+    const uint32_t stage0 = smem_addr(s_stage), plane0 = smem_addr(s_plane);
+
     const int64_t lo = clamp_row(p.offsets[e], p.R), hi = clamp_row(p.offsets[e + 1], p.R);
+    const int rows = hi > lo ? (int)(hi - lo) : 0;
     const float scal = d.factor && p.scaling ? __ldg(p.scaling + e) : 1.0f;
+    // stage i of this CTA: rows first(i) .. first(i) + SR - 1 of the adapter
+    const int stages = (rows + SR * CS - 1) / (SR * CS);
+    auto first = [&](int i) { return (i * CS + crank) * SR; };
+
+    // the row of `right` behind row `local` of the adapter, or -1
+    auto source_row = [&](int local) -> int {
+        if (local >= rows) return -1;
+        const int64_t r = lo + local;
+        const int64_t at = d.row ? (int64_t)__ldg(d.row + r) : r;
+        return at >= 0 && at < d.n ? (int)at : -1;
+    };
+    auto issue = [&](int i) {
+        constexpr int CPR = (Q8 ? CW : 2 * CW) / 16;       // 16-byte pieces of a row
+        const int* row = s_row + (i & 1) * SR;
+        const uint32_t dst = stage0 + (uint32_t)((i % kGradStages) * S::stage_bytes);
+        const int per = Q8 ? 16 : 8;
+#pragma unroll
+        for (int q = 0; q < SR * CPR / kLoraThreads; ++q) {
+            const int id = q * kLoraThreads + tid, r = id / CPR, c = id % CPR;
+            const int at = row[r];
+            const bool ok = at >= 0 && col0 + c * per < d.C;
+            const void* src = Q8 ? (const void*)(d.codes + (ok ? (int64_t)at * d.C + col0 + c * per : 0))
+                                 : (const void*)(d.right + (ok ? (int64_t)at * d.C + col0 + c * per : 0));
+            copy_async16(dst + (uint32_t)(r * (Q8 ? S::kPitch8 : S::kPitch16) + c * 16), src, ok ? 16u : 0u);
+        }
+    };
+
+    // `left` of the next stage, in registers until the stage before it is being worked on
+    float4 left[S::kLeft];
+    float fac[S::kLeft];
+    uint32_t scale[(SR * (CW / 32) + kLoraThreads - 1) / kLoraThreads];
+    auto fetch = [&](int i) {
+#pragma unroll
+        for (int q = 0; q < S::kLeft; ++q) {
+            const int id = q * kLoraThreads + tid, local = first(i) + id / (RP / 4), j = 4 * (id % (RP / 4));
+            left[q] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            fac[q] = scal;
+            if (id < SR * RP / 4 && local < rows && j < p.r) {
+                const int64_t r = lo + local;
+                left[q] = __ldg(reinterpret_cast<const float4*>(d.left + r * p.r + j));
+                if (d.factor && p.weight) fac[q] *= __ldg(p.weight + r);
+            }
+        }
+        if constexpr (Q8) {
+            constexpr int BPR = CW / 32;
+#pragma unroll
+            for (int q = 0; q < (SR * BPR + kLoraThreads - 1) / kLoraThreads; ++q) {
+                const int id = q * kLoraThreads + tid;
+                scale[q] = 0u;
+                if (id < SR * BPR && col0 + 32 * (id % BPR) < d.C) {
+                    const int at = source_row(first(i) + id / BPR);
+                    if (at >= 0) scale[q] = __ldg(d.scales + (int64_t)at * (d.C / 32) + col0 / 32 + id % BPR);
+                }
+            }
+        }
+    };
+    auto place = [&](int i) {
+        uint16_t* plane = s_plane + (i & 1) * (S::plane_bytes / 2);
+#pragma unroll
+        for (int q = 0; q < S::kLeft; ++q) {
+            const int id = q * kLoraThreads + tid;
+            if (id < SR * RP / 4) {
+                uint32_t a[TERMS], b[TERMS];
+                split_pair<TERMS, false>(left[q].x * fac[q], left[q].y * fac[q], a);
+                split_pair<TERMS, false>(left[q].z * fac[q], left[q].w * fac[q], b);
+#pragma unroll
+                for (int k = 0; k < TERMS; ++k)
+                    *reinterpret_cast<uint2*>(plane + (size_t)(k * SR + id / (RP / 4)) * S::kPlane + 4 * (id % (RP / 4))) =
+                        make_uint2(a[k], b[k]);
+            }
+        }
+        if constexpr (Q8) {
+#pragma unroll
+            for (int q = 0; q < (SR * (CW / 32) + kLoraThreads - 1) / kLoraThreads; ++q) {
+                const int id = q * kLoraThreads + tid;
+                if (id < SR * (CW / 32)) s_scale[(i & 1) * S::scale_bytes + id] = (uint8_t)scale[q];
+            }
+        }
+    };
 
     float acc[MT][CT][4];
 #pragma unroll
@@ -594,84 +702,113 @@ __device__ __forceinline__ void grad_body(const LoraGradArgs& p, const LoraGradS
 #pragma unroll
             for (int j = 0; j < 4; ++j) acc[m][c][j] = 0.0f;
 
-    for (int64_t base = lo + 16 * (wr + (int64_t)WR * crank); base < hi; base += 16 * WR * CS) {
-        // this lane's four contraction rows: base + 4t .. 4t+3
-        uint32_t x[4][CT / 2];
-        float fac[4];
+    // prologue: two stages of copies under way, the first stage's left in place
+    static_assert(kGradStages == 3, "the prologue and the row buffers are written for three stages");
+    if (tid < SR) {
+        s_row[tid] = source_row(first(0) + tid);
+        s_row[SR + tid] = source_row(first(1) + tid);
+    }
+    fetch(0);
+    __syncthreads();
+    if (stages > 0) issue(0);
+    copy_commit();
+    if (stages > 1) issue(1);
+    copy_commit();
+    place(0);
+    fetch(1);
+    int next_row = tid < SR ? source_row(first(2) + tid) : -1;
+    __syncthreads();                                    // s_row has been read
+    if (tid < SR) s_row[tid] = next_row;                // stage 2's
+    next_row = tid < SR ? source_row(first(3) + tid) : -1;
+
+    for (int i = 0; i < stages; ++i) {
+        copy_wait<1>();
+        __syncthreads();                                // stage i is there; stage i - 1 is done with
+        if (i + 2 < stages) issue(i + 2);
+        copy_commit();
+        place(i + 1);
+        if (tid < SR) s_row[((i + 3) & 1) * SR + tid] = next_row;
+        fetch(i + 2);
+        next_row = tid < SR ? source_row(first(i + 4) + tid) : -1;
+
+        const uint32_t x = stage0 + (uint32_t)((i % kGradStages) * S::stage_bytes);
+        const uint32_t plane = plane0 + (uint32_t)((i & 1) * S::plane_bytes);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int64_t r = base + 4 * t + i;
-#pragma unroll
-            for (int w = 0; w < CT / 2; ++w) x[i][w] = 0u;
-            fac[i] = 0.0f;
-            if (r < hi) {
-                fac[i] = d.factor && p.weight ? scal * __ldg(p.weight + r) : scal;
-                const int64_t at = d.row ? (int64_t)__ldg(d.row + r) : r;
-                if (in && at >= 0 && at < d.n) {
-                    if constexpr (Q8) {
-                        const float step = act8_step(__ldg(d.scales + at * (d.C / 32) + (col >> 5)));
-                        uint2 q;
-                        if constexpr (CT == 8) q = __ldg(reinterpret_cast<const uint2*>(d.codes + at * d.C + col));
-                        else q = make_uint2(__ldg(reinterpret_cast<const uint32_t*>(d.codes + at * d.C + col)), 0u);
-                        float f[8];
-                        act8_values(q, step, f);
-#pragma unroll
-                        for (int w = 0; w < CT / 2; ++w) x[i][w] = pack_bf16x2(f[2 * w], f[2 * w + 1]);
-                    } else if constexpr (CT == 8) {
-                        const uint4 v = ldg16(d.right + at * d.C + col);
-                        x[i][0] = v.x, x[i][1] = v.y, x[i][2] = v.z, x[i][3] = v.w;
-                    } else {
-                        const uint2 v = ldg8(d.right + at * d.C + col);
-                        x[i][0] = v.x, x[i][1] = v.y;
-                    }
-                }
-            }
-        }
-        uint32_t a[MT][4][TERMS];
-#pragma unroll
-        for (int m = 0; m < MT; ++m)
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const int j = 16 * m + 8 * h + g;
-                float v[4];
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int64_t r = base + 4 * t + i;
-                    v[i] = r < hi && j < p.r ? fac[i] * __ldg(d.left + r * p.r + j) : 0.0f;
-                }
-                uint32_t o[TERMS];
-                split_pair<TERMS, false>(v[0], v[1], o);
-#pragma unroll
-                for (int q = 0; q < TERMS; ++q) a[m][h][q] = o[q];
-                split_pair<TERMS, false>(v[2], v[3], o);
-#pragma unroll
-                for (int q = 0; q < TERMS; ++q) a[m][2 + h][q] = o[q];
-            }
-#pragma unroll
-        for (int c = 0; c < CT; ++c) {
-            const uint32_t sel = (c & 1) ? 0x7632u : 0x5410u;
-            const uint32_t b0 = prmt(x[0][c / 2], x[1][c / 2], sel), b1 = prmt(x[2][c / 2], x[3][c / 2], sel);
+        for (int half = 0; half < 2; ++half) {
+            const int r0 = 32 * wr + 16 * half;
+            uint32_t a[MT][TERMS][4];
 #pragma unroll
             for (int m = 0; m < MT; ++m)
 #pragma unroll
-                for (int q = 0; q < TERMS; ++q)
-                    mma_bf16_16816(acc[m][c], a[m][0][q], a[m][1][q], a[m][2][q], a[m][3][q], b0, b1);
+                for (int k = 0; k < TERMS; ++k)
+                    ldmatrix4_trans(a[m][k], plane + (uint32_t)(((k * SR + r0 + (lane & 7) + 8 * (lane >> 4)) * S::kPlane +
+                                                                 16 * m + 8 * ((lane >> 3) & 1)) * 2));
+            if constexpr (!Q8) {
+#pragma unroll
+                for (int c = 0; c < CT; c += 2) {
+                    uint32_t b[4];                       // two column tiles: rows 0-7 and 8-15 of each
+                    ldmatrix4_trans(b, x + (uint32_t)((r0 + (lane & 15)) * S::kPitch16 +
+                                                      (wc * S::SC + 8 * c + 8 * (lane >> 4)) * 2));
+#pragma unroll
+                    for (int m = 0; m < MT; ++m)
+#pragma unroll
+                        for (int k = 0; k < TERMS; ++k) {
+                            mma_bf16_16816(acc[m][c], a[m][k][0], a[m][k][1], a[m][k][2], a[m][k][3], b[0], b[1]);
+                            mma_bf16_16816(acc[m][c + 1], a[m][k][0], a[m][k][1], a[m][k][2], a[m][k][3], b[2], b[3]);
+                        }
+                }
+            } else {
+                // this lane's rows 2t, 2t+1, 2t+8, 2t+9, its CT columns from CT g on
+                uint32_t v[4][CT / 2];
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    const int row = r0 + 2 * t + (r & 1) + 8 * (r >> 1);
+                    const uint8_t* at = s_stage + (i % kGradStages) * S::stage_bytes + row * S::kPitch8 + wc * S::SC + CT * g;
+                    uint2 q;
+                    if constexpr (CT == 8) q = *reinterpret_cast<const uint2*>(at);
+                    else q = make_uint2(*reinterpret_cast<const uint32_t*>(at), 0u);
+                    const float step = act8_step(s_scale[(i & 1) * S::scale_bytes + row * (CW / 32) + (wc * S::SC + CT * g) / 32]);
+                    float f[8];
+                    act8_values(q, step, f);
+#pragma unroll
+                    for (int w = 0; w < CT / 2; ++w) v[r][w] = pack_bf16x2(f[2 * w], f[2 * w + 1]);
+                }
+#pragma unroll
+                for (int c = 0; c < CT; ++c) {
+                    const uint32_t sel = (c & 1) ? 0x7632u : 0x5410u;
+                    const uint32_t b0 = prmt(v[0][c / 2], v[1][c / 2], sel), b1 = prmt(v[2][c / 2], v[3][c / 2], sel);
+#pragma unroll
+                    for (int m = 0; m < MT; ++m)
+#pragma unroll
+                        for (int k = 0; k < TERMS; ++k)
+                            mma_bf16_16816(acc[m][c], a[m][k][0], a[m][k][1], a[m][k][2], a[m][k][3], b0, b1);
+                }
+            }
         }
     }
-    // MMA tile c, column index n of the accumulators is slab column CT n + c
+    copy_wait<0>();
+    __syncthreads();                                     // the stages become the sums' space
+
+    // column of the accumulators: tile c, MMA column n is 8 c + n, from codes CT n + c
+    float* s_red = reinterpret_cast<float*>(smem);
     float* mine = s_red + (size_t)warp * RP * S::kStride;
 #pragma unroll
     for (int m = 0; m < MT; ++m)
 #pragma unroll
         for (int h = 0; h < 2; ++h)
 #pragma unroll
-            for (int c = 0; c < CT; ++c)
-#pragma unroll
-                for (int i = 0; i < 2; ++i)
-                    mine[(16 * m + 8 * h + g) * S::kStride + CT * (2 * t + i) + c] = acc[m][c][2 * h + i];
+            for (int c = 0; c < CT; ++c) {
+                float* row = mine + (16 * m + 8 * h + g) * S::kStride;
+                if constexpr (Q8) {
+                    row[CT * (2 * t) + c] = acc[m][c][2 * h];
+                    row[CT * (2 * t + 1) + c] = acc[m][c][2 * h + 1];
+                } else {
+                    *reinterpret_cast<float2*>(row + 8 * c + 2 * t) = make_float2(acc[m][c][2 * h], acc[m][c][2 * h + 1]);
+                }
+            }
     __syncthreads();
     if (WR > 1) {
-        for (int i = tid; i < WC * RP * S::SC; i += kLoraThreads) {
+        for (int i = tid; i < CW * RP; i += kLoraThreads) {
             const int w = i / (RP * S::SC), at = (i / S::SC % RP) * S::kStride + i % S::SC;
             float v = s_red[(size_t)w * RP * S::kStride + at];
 #pragma unroll
@@ -685,13 +822,13 @@ __device__ __forceinline__ void grad_body(const LoraGradArgs& p, const LoraGradS
         cluster_wait();
     }
     // the cluster's CTAs share the elements out
-    const int share = (WC * RP * S::SC + CS - 1) / CS;
-    const int i1 = min((crank + 1) * share, WC * RP * S::SC);
+    const int share = (CW * RP + CS - 1) / CS;
+    const int i1 = min((crank + 1) * share, CW * RP);
     for (int i = crank * share + tid; i < i1; i += kLoraThreads) {
         const int w = i / (RP * S::SC), q = i % (RP * S::SC);
         // consecutive threads along the gradient's contiguous axis: its columns (dA) or the rank (dB)
         const int j = d.transposed ? q % RP : q / S::SC, n = d.transposed ? q / RP : q % S::SC;
-        const int c = (slab0 + w) * S::SC + n;
+        const int c = col0 + w * S::SC + n;
         if (j >= p.r || c >= d.C) continue;
         const float* at = s_red + (size_t)w * RP * S::kStride + j * S::kStride + n;
         float v = 0.0f;
@@ -703,7 +840,7 @@ __device__ __forceinline__ void grad_body(const LoraGradArgs& p, const LoraGradS
         if (TERMS == 3) reinterpret_cast<float*>(d.out)[o] = v;
         else reinterpret_cast<uint16_t*>(d.out)[o] = f32_to_bf16_rne(v);
     }
-    if (CS > 1) {
+    if (CS > 1) {                                        // a CTA's sums are read until here
         cluster_arrive();
         cluster_wait();
     }
@@ -715,33 +852,33 @@ __host__ __device__ __forceinline__ int grad_items(const LoraGradSide& d, int co
 }
 
 template <int RP, int WR, int TERMS, bool Q8>
-__global__ void __launch_bounds__(kLoraThreads, RP <= 16 ? 2 : 1) lora_grads_kernel(const LoraGradArgs p) {
-    extern __shared__ __align__(16) float s_red[];
-    constexpr int WC = kLoraWarps / WR;
+__global__ void __launch_bounds__(kLoraThreads, RP <= 32 && WR == 1 ? 2 : 1) lora_grads_kernel(const LoraGradArgs p) {
+    extern __shared__ __align__(16) uint8_t smem[];
+    constexpr int CW = GradShape<RP, WR, TERMS>::CW;
     const int item = (int)(blockIdx.x / cluster_size());
-    const int na = grad_items(p.a, GradShape<RP>::SC * WC), nb = grad_items(p.b, GradShape<RP>::SC * WC);
+    const int na = grad_items(p.a, CW), nb = grad_items(p.b, CW);
     const int e = item / (na + nb), i = item % (na + nb);
-    if (i < na) grad_body<RP, WR, TERMS, Q8>(p, p.a, e, i * WC, s_red);
-    else grad_body<RP, WR, TERMS, false>(p, p.b, e, (i - na) * WC, s_red);
+    if (i < na) grad_body<RP, WR, TERMS, Q8>(p, p.a, e, i * CW, smem);
+    else grad_body<RP, WR, TERMS, false>(p, p.b, e, (i - na) * CW, smem);
 }
 
 template <int RP, int WR, int TERMS, bool Q8>
 cudaError_t launch_grads_t(const LoraGradArgs& a, int cs, cudaStream_t s) {
-    constexpr size_t smem = grads_smem<RP>();
+    using S = GradShape<RP, WR, TERMS>;
+    static_assert(S::smem <= 227 * 1024, "shared memory of a CTA");
     static std::atomic<bool> attr_set[64];
     const int dev = current_device();
     if (!attr_set[dev].load(std::memory_order_acquire)) {
         const cudaError_t e = cudaFuncSetAttribute(lora_grads_kernel<RP, WR, TERMS, Q8>,
-                                                   cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+                                                   cudaFuncAttributeMaxDynamicSharedMemorySize, (int)S::smem);
         if (e != cudaSuccess) return e;
         attr_set[dev].store(true, std::memory_order_release);
     }
-    constexpr int cols = GradShape<RP>::SC * (kLoraWarps / WR);
-    const int64_t items = (int64_t)a.L * (grad_items(a.a, cols) + grad_items(a.b, cols));
+    const int64_t items = (int64_t)a.L * (grad_items(a.a, S::CW) + grad_items(a.b, S::CW));
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(items * cs));
     cfg.blockDim = dim3(kLoraThreads);
-    cfg.dynamicSmemBytes = smem;
+    cfg.dynamicSmemBytes = S::smem;
     cfg.stream = s;
     cudaLaunchAttribute at[1];
     at[0].id = cudaLaunchAttributeClusterDimension;
@@ -761,13 +898,19 @@ cudaError_t launch_grads_w(const LoraGradArgs& a, bool f32, int cs, cudaStream_t
 
 template <int RP>
 cudaError_t launch_grads_r(const LoraGradArgs& a, bool f32, cudaStream_t s) {
-    // warps along the rows of an adapter until each has about 128 of them
+    // warps and then CTAs along the rows where the columns and adapters alone leave SMs idle
+    constexpr int WR = RP <= 64 ? 4 : 2;
     const int64_t active = a.R < a.L ? (a.R > 0 ? a.R : 1) : a.L;
     const int64_t avg = (a.R + active - 1) / active;
-    if (avg <= 512) return launch_grads_w<RP, 2>(a, f32, 1, s);
+    const int wide = GradShape<RP, 1, 2>::CW;
+    const int64_t sms = device_sm_count();
+    if (avg <= 64 || active * (grad_items(a.a, wide) + grad_items(a.b, wide)) >= 2 * sms)
+        return launch_grads_w<RP, 1>(a, f32, 1, s);
+    const int cols = GradShape<RP, WR, 2>::CW;
+    const int64_t items = active * (grad_items(a.a, cols) + grad_items(a.b, cols));
     int cs = 1;
-    while (cs < 8 && avg > 1024 * cs) cs *= 2;
-    return launch_grads_w<RP, 8>(a, f32, cs, s);
+    while (cs < 8 && items * cs * 2 <= sms && avg >= 2 * cs * GradShape<RP, WR, 2>::SR) cs *= 2;
+    return launch_grads_w<RP, WR>(a, f32, cs, s);
 }
 
 // bits: 1 offsets decrease or leave [0, R], 2 offsets[0] != 0, 4 and 8 a row index of the rows

@@ -368,7 +368,7 @@ gnf4_status gnf4_combine_topk(const void* y, int64_t R, int64_t N, const int32_t
  *
  * gnf4_quantize_act8 writes the checkpoint of x, gnf4_dequantize_act8 reads one back.
  * x, out device bf16 [rows, K], 16-byte aligned
- * codes  device int8  [rows, K], 8-byte aligned
+ * codes  device int8  [rows, K], 16-byte aligned
  * scales device uint8 [rows, K/32]
  * rows >= 0, K % 32 == 0. One kernel launch; rows == 0 launches nothing and accepts NULL
  * buffers. Outputs may not overlap inputs.
@@ -383,7 +383,7 @@ gnf4_status gnf4_dequantize_act8(const int8_t* codes, const uint8_t* scales, int
  * gnf4_swiglu that also writes the checkpoint of its gate_up rows, in one pass over them:
  * out is gnf4_swiglu's bit for bit, codes and scales are gnf4_quantize_act8's of gate_up.
  * gate_up device bf16 [R, 2I], 16-byte aligned; out device bf16 [R, I], 16-byte aligned;
- * codes device int8 [R, 2I], 8-byte aligned; scales device uint8 [R, 2I/32]. I % 32 == 0.
+ * codes device int8 [R, 2I], 16-byte aligned; scales device uint8 [R, 2I/32]. I % 32 == 0.
  * One kernel launch; R == 0 launches nothing and accepts NULL buffers.
  */
 gnf4_status gnf4_swiglu_act8(const void* gate_up, int64_t R, int64_t I, void* out, int8_t* codes,
@@ -400,7 +400,7 @@ gnf4_status gnf4_swiglu_act8(const void* gate_up, int64_t R, int64_t I, void* ou
  * scales. Computed in fp32 (relative error about 2^-17 of |d up sig| (1 + |gate|) and of
  * |d gate sig| before the rounding; finite gates).
  * grad_out device bf16 [R, I]; gate_up device bf16 [R, 2I] or NULL; codes device int8 [R, 2I]
- * (8-byte aligned) and scales device uint8 [R, 2I/32], given exactly if gate_up is not;
+ * (16-byte aligned) and scales device uint8 [R, 2I/32], given exactly if gate_up is not;
  * grad_gate_up device bf16 [R, 2I]; act device bf16 [R, I] or NULL. bf16 buffers are 16-byte
  * aligned; outputs may not overlap inputs. I % 8 == 0 (I % 32 == 0 with a checkpoint).
  * One kernel launch; R == 0 launches nothing and accepts NULL buffers.
@@ -434,8 +434,9 @@ gnf4_status gnf4_swiglu_backward(const void* grad_out, const void* gate_up, cons
  *            a row whose token or destination is out of range counts as zeros or is not written
  * scaling    device fp32 [L], or NULL
  * h          device fp32 [R, r], or NULL: the rows h, which gnf4_lora_backward wants
- * L in [1, 2048], r in [8, 128] with r % 8 == 0, K % 8 == 0, N % 8 == 0. 16-bit buffers are
- * 16-byte aligned, fp32 and int32 ones 4-byte, offsets 8-byte. Sums in fp32; h enters the
+ * L in [1, 2048], r in [8, 128] with r % 8 == 0, K and N multiples of 8 up to 2^24, R at most
+ * 2^30. 16-bit buffers and h are
+ * 16-byte aligned, row arrays and scaling 4-byte, offsets 8-byte. Sums in fp32; h enters the
  * second product with about 17 significant bits (two 16-bit terms). Deterministic: the same
  * call gives the same bits. R == 0 launches nothing and accepts NULL buffers.
  * flags: 0 or GNF4_CHECK (validates offsets, row arrays and weights on the device first: one
@@ -459,7 +460,7 @@ gnf4_status gnf4_lora_apply(const void* base, const void* x, int dtype, const vo
  * zeros), and gnf4_combine_topk sums a token's rows afterwards. dA and dB are written for
  * every adapter; one without rows gets zeros.
  * grad_out   device bf16 [T_g, N]
- * x          device bf16 [T_in, K], or NULL: then x_codes int8 [T_in, K] (8-byte aligned) and
+ * x          device bf16 [T_in, K], or NULL: then x_codes int8 [T_in, K] (16-byte aligned) and
  *            x_scales uint8 [T_in, K/32] hold its checkpoint (K % 32 == 0)
  * h          device fp32 [R, r] as the forward wrote it
  * dx         device bf16 [R, K], may be dx_base; or NULL (with dx_base NULL): not wanted

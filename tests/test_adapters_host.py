@@ -38,7 +38,7 @@ COMMON = [
     (dict(K=(1 << 24) + 8), SHAPE), (dict(R=1 << 31, T_in=1 << 31), SHAPE),
     (dict(x=FAKE + 8), MISALIGNED), (dict(A=FAKE + 2), MISALIGNED), (dict(B=FAKE + 8), MISALIGNED),
     (dict(off=FAKE + 4), MISALIGNED), (dict(tok=FAKE + 2), MISALIGNED), (dict(wt=FAKE + 1), MISALIGNED),
-    (dict(scal=FAKE + 2), MISALIGNED), (dict(h=FAKE + 2), MISALIGNED),
+    (dict(scal=FAKE + 2), MISALIGNED), (dict(h=FAKE + 8), MISALIGNED),
 ]
 
 
@@ -59,8 +59,8 @@ def test_apply_refusals(kw, status):
     (dict(dx=None), INVALID),                                # dx_base without dx
     (dict(T_g=7), INVALID), (dict(xc=FAKE, xs=FAKE), INVALID), (dict(x=None, xc=FAKE), INVALID),
     (dict(x=None, xs=FAKE), INVALID), (dict(x=None, xc=FAKE, xs=FAKE, K=264), SHAPE),
-    (dict(x=None, xc=FAKE + 4, xs=FAKE), MISALIGNED), (dict(g=FAKE + 2), MISALIGNED), (dict(dx=FAKE + 8), MISALIGNED),
-    (dict(dA=FAKE + 2), MISALIGNED), (dict(dB=FAKE + 8), MISALIGNED), (dict(gh=FAKE + 2), MISALIGNED),
+    (dict(x=None, xc=FAKE + 8, xs=FAKE), MISALIGNED), (dict(g=FAKE + 2), MISALIGNED), (dict(dx=FAKE + 8), MISALIGNED),
+    (dict(dA=FAKE + 2), MISALIGNED), (dict(dB=FAKE + 8), MISALIGNED), (dict(gh=FAKE + 8), MISALIGNED),
     (dict(src=FAKE + 2), MISALIGNED), (dict(), INVALID), (dict(R=0, off=None), INVALID),
 ])
 def test_backward_refusals(kw, status):
@@ -72,7 +72,7 @@ def test_backward_refusals(kw, status):
     (dict(gh=None), INVALID), (dict(x=None), INVALID), (dict(x=None, xc=FAKE), INVALID), (dict(xc=FAKE), INVALID),
     (dict(off=None), INVALID), (dict(dA=None), INVALID), (dict(T_in=7), INVALID), (dict(L=0), INVALID),
     (dict(flags=2), INVALID), (dict(gdt=1), INVALID), (dict(r=12), SHAPE), (dict(K=252), SHAPE),
-    (dict(x=None, xc=FAKE, xs=FAKE, K=264), SHAPE), (dict(gh=FAKE + 2), MISALIGNED), (dict(x=FAKE + 8), MISALIGNED),
+    (dict(x=None, xc=FAKE, xs=FAKE, K=264), SHAPE), (dict(gh=FAKE + 8), MISALIGNED), (dict(x=FAKE + 8), MISALIGNED),
     (dict(dA=FAKE + 8), MISALIGNED), (dict(off=FAKE + 4), MISALIGNED), (dict(tok=FAKE + 2), MISALIGNED),
     (dict(), INVALID),
 ])
@@ -95,7 +95,7 @@ def test_act8_refusals():
         assert f(FAKE, 4, 48, FAKE, FAKE) == SHAPE
         assert f(FAKE, 1 << 60, 1 << 10, FAKE, FAKE) == SHAPE
         assert f(FAKE + 8, 4, 64, FAKE, FAKE) == MISALIGNED
-        assert f(FAKE, 4, 64, FAKE + 4, FAKE) == MISALIGNED
+        assert f(FAKE, 4, 64, FAKE + 8, FAKE) == MISALIGNED
         assert f(FAKE, 4, 64, FAKE, FAKE + 1) == INVALID         # any alignment, but not device memory
         assert f(None, 0, 64, None, None) == OK
     buf = (ctypes.c_uint16 * 1024)()
