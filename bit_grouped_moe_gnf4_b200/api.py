@@ -21,13 +21,16 @@ def _stream(stream) -> int:
     """A torch.cuda.Stream, a raw cudaStream_t handle as an int (0 = the legacy default
     stream), or None for torch's current stream."""
     if stream is None:
-        stream = torch.cuda.current_stream()
+        # the handle itself: torch.cuda.current_stream() first makes a Stream object (3 us a call)
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
 
 
 def _need(t: torch.Tensor, dtype: torch.dtype, name: str) -> None:
+    if type(t) is torch.Tensor and t.dtype is dtype and t.is_contiguous():
+        return
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if t.dtype != dtype:
@@ -309,9 +312,11 @@ def combine_topk(y: torch.Tensor, T: int, k: int, row_of_slot: Optional[torch.Te
 def _shaped(t: Optional[torch.Tensor], shape, dtype: torch.dtype, name: str, like: torch.Tensor) -> torch.Tensor:
     """``t`` checked against a type and shape, or a new tensor beside ``like`` if it is None."""
     if t is None:
-        return torch.empty(shape, dtype=dtype, device=like.device)
+        if like.dtype is dtype:
+            return torch.empty_like(like) if like.shape == shape else like.new_empty(shape)
+        return like.new_empty(shape, dtype=dtype)
     _need(t, dtype, name)
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape:
         raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
     return t
 

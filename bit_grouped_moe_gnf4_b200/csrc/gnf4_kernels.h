@@ -121,5 +121,6 @@ int current_device();
 // on a barrier (synchronous; 0 = no event). Returns a CUDA error through *err.
 unsigned take_decode_error(cudaError_t* err);
 unsigned take_prefill_error(cudaError_t* err);
+unsigned take_lora_error(cudaError_t* err);
 
 }  // namespace gnf4

@@ -8,6 +8,8 @@ also when an addition truncates instead of rounding, and every operand that is s
 2^-24. So with n = K + r (forward), N + r (dx), N + rows (dA), rows (dB), plus 32 for the
 handful of products and joins on the way:
     |out - want| <= u |want| + (1 + u) (n 2^-23 + 2^-16) bound, and half a step of the type's subnormals
+A base on top may be where the fp32 accumulation of the second product starts: r/8 additions
+(two terms, 16 ranks each) of 2^-23 of it.
 """
 import numpy as np
 import pytest
@@ -35,10 +37,10 @@ def f64(t):
     return None if t is None else t.double().cpu().numpy()
 
 
-def near(got, want, bound, n, terms, what):
+def near(got, want, bound, n, terms, what, base=0.0, r=0):
     u = HALF[got.dtype]
     e = n * 2.0 ** -23 + (2.0 ** -16 if terms == 2 else 2.0 ** -24)
-    tol = u * np.abs(want) + (1 + u) * e * bound + TINY[got.dtype]
+    tol = u * np.abs(want) + (1 + u) * (e * bound + (r / 8 + 2) * 2.0 ** -23 * np.abs(base)) + TINY[got.dtype]
     err = np.abs(f64(got) - want)
     assert np.all(err <= tol), f"{what}: {int((err > tol).sum())} of {err.size} off, worst {float((err / tol).max()):.3g} of the bound"
 
@@ -87,7 +89,7 @@ class Problem:
                                             self.offsets.cpu().numpy(), row_dest=None if self.dest is None else
                                             self.dest[:self.R].cpu().numpy(), **self.host())
         K, r = self.A.shape[2], self.A.shape[1]
-        near(out, want, bound, K + r + 32, 2, "out")
+        near(out, want, bound, K + r + 32, 2, "out", f64(self.base), r)
         hb = np.abs(f64(self.x))[self.host()["row_token"] if self.tok is not None else slice(0, self.R)].max() * \
             np.abs(f64(self.A)).sum(axis=2).max()
         near(h[:self.R], wh, np.full_like(wh, hb), K + 32, 3, "h")
@@ -121,7 +123,7 @@ class Problem:
         m = int(np.diff(self.offsets.cpu().numpy()).max())
         terms = 3 if grads == torch.float32 else 2
         near(gh[:self.R], w["grad_h"], w["grad_h_bound"], N + 32, 3, "grad_h")
-        near(dx[:self.R], w["dx"], w["dx_bound"], N + r + 32, 2, "dx")
+        near(dx[:self.R], w["dx"], w["dx_bound"], N + r + 32, 2, "dx", 0.0 if dxb is None else f64(dxb)[:self.R], r)
         near(out[1], w["dA"], w["dA_bound"], N + m + 32, terms, "dA")
         near(out[2], w["dB"], w["dB_bound"], m + 32, terms, "dB")
         return out
@@ -182,6 +184,41 @@ def test_backward_without_each_array(kw):
     for counts in ([3, 0, 20], [60, 1]):
         Problem(counts, 16, 264, 200, **kw).check_backward()
         Problem(counts, 16, 264, 200, **kw).check_backward(base=False)
+
+
+LARGE = {"one": [2500], "several": [900, 0, 1, 700, 1000, 0], "many": [25] * 100, "more": [61] * 170,
+         "skewed": [9000] + [i % 4 for i in range(200)]}
+
+
+@pytest.mark.parametrize("counts", list(LARGE))
+@pytest.mark.parametrize("r,K,N", [(16, 256, 192), (8, 72, 40), (24, 520, 136), (64, 264, 776), (40, 1032, 512), (128, 200, 264)])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+def test_many_rows(counts, r, K, N, dtype):
+    p = Problem(LARGE[counts], r, K, N, dtype=dtype, seed=r, spare=3)
+    p.check_forward()
+    if dtype == torch.bfloat16:
+        p.check_backward(torch.float32, act8=K % 32 == 0)
+
+
+def test_many_rows_without_arrays_and_with_bad_ones():
+    p = Problem([2600, 0, 77], 16, 264, 200, gather=False, scatter=False, weights=False, scaling=False)
+    p.check_forward()
+    p.check_backward(base=False)
+    p = Problem([2600, 0, 77], 32, 96, 72)
+    ok, _ = p.forward()
+    dest = p.dest.clone()
+    p.tok[2], p.dest[2677 - 1] = len(p.x), -1
+    p.x[5] = float("nan")                                # one token's rows
+    out, _ = p.forward()
+    hit = (p.tok == 5)
+    want = ok.clone()
+    want[dest[-1].long()] = p.base[dest[-1].long()]
+    want[dest[2].long()] = p.base[dest[2].long()]
+    rest = torch.ones(len(out), dtype=torch.bool, device="cuda")
+    rest[dest[hit].long()] = False
+    assert torch.equal(out[rest], want[rest])
+    hit[-1] = False
+    assert out[dest[hit].long()].isnan().all()
 
 
 def test_long_segments_split_over_a_cluster():
@@ -439,7 +476,7 @@ def test_requests_through_routing_metadata():
             h = f64(A[e]) @ f64(x[i])
             want[i] += f64(B[e]) @ h
             bound[i] = (np.abs(f64(A[e])) @ np.abs(f64(x[i]))).max() * np.abs(f64(B[e])).sum(axis=1)
-    near(y, want, bound, K + r + 32, 2, "y")
+    near(y, want, bound, K + r + 32, 2, "y", f64(base), r)
     gone = ids[:, 0] < 0
     assert gone.any() and torch.equal(y[gone], base[gone])
 
@@ -489,9 +526,9 @@ def test_expert_layer_trains_its_adapters():
 
     o, tk, ds, ww = (v.cpu().numpy() for v in (off, tok, dst, w))
     want, wh, b = LO.lora_apply_f64(f64(gu0), f64(x), f64(A1), f64(B1), o, row_token=tk, scaling=f64(s1))
-    near(gu, want, b, H + r + 32, 2, "gate_up")
+    near(gu, want, b, H + r + 32, 2, "gate_up", f64(gu0), r)
     want, _, b = LO.lora_apply_f64(f64(y0), f64(act), f64(A2), f64(B2), o, row_weight=ww, row_dest=ds, scaling=f64(s2))
-    near(y, want, b, I + r + 32, 2, "down")
+    near(y, want, b, I + r + 32, 2, "down", f64(y0), r)
     xb, gb = x.view(torch.int16).cpu().numpy().view(np.uint16), dout.view(torch.int16).cpu().numpy().view(np.uint16)
     # against the exact layer the rounded intermediate rows leave a few bf16 steps of each row's largest value
     exact_gu = O.grouped_rows_f64("nf4", xb, Wh, Sh, o, tk, None, H, np.arange(R))
@@ -500,7 +537,7 @@ def test_expert_layer_trains_its_adapters():
     bw = LO.lora_backward_f64(f64(dout), f64(act_again), f64(h2), f64(A2), f64(B2), o, row_src=tk, row_weight=ww,
                               scaling=f64(s2), dx_base=f64(d_act0))
     m = int(np.diff(o).max())
-    near(d_act, bw["dx"], bw["dx_bound"], H + r + 32, 2, "d_act")
+    near(d_act, bw["dx"], bw["dx_bound"], H + r + 32, 2, "d_act", f64(d_act0), r)
     near(dA2, bw["dA"], bw["dA_bound"], H + m + 32, 2, "dA of down")
     near(dB2, bw["dB"], bw["dB_bound"], m + 32, 2, "dB of down")
     gu8 = A8.values_act8(codes.cpu().numpy(), scales.cpu().numpy())
@@ -510,7 +547,7 @@ def test_expert_layer_trains_its_adapters():
     assert np.all(np.abs(f64(act_again) - want) <= (2.0 ** -8 + 2.0 ** -16) * np.abs(want) + 2.0 ** -118)
     bw = LO.lora_backward_f64(f64(d_gu), A8.values_act8(xq[0].cpu().numpy(), xq[1].cpu().numpy()), f64(h1), f64(A1),
                               f64(B1), o, row_token=tk, scaling=f64(s1), dx_base=f64(dx0))
-    near(dx, bw["dx"], bw["dx_bound"], 2 * I + r + 32, 2, "dx")
+    near(dx, bw["dx"], bw["dx_bound"], 2 * I + r + 32, 2, "dx", f64(dx0), r)
     near(dA1, bw["dA"], bw["dA_bound"], 2 * I + m + 32, 2, "dA of gate_up")
     near(dB1, bw["dB"], bw["dB_bound"], m + 32, 2, "dB of gate_up")
     ref = D.dgrad_rows_f64("mxfp4", gb, Vh, Uh, o, tk, ww, np.arange(R))
