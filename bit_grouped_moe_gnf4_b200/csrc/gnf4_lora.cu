@@ -176,6 +176,11 @@ __device__ __forceinline__ uint4 lds16(uint32_t a) {
     asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a) : "memory");
     return v;
 }
+__device__ __forceinline__ uint32_t lds4(uint32_t a) {
+    uint32_t v;
+    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
+    return v;
+}
 __device__ __forceinline__ uint2 lds8(uint32_t a) {
     uint2 v;
     asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a) : "memory");
@@ -1108,7 +1113,7 @@ struct GradShape {
     static constexpr int kLeft = (SR * RP / 4 + kLoraThreads - 1) / kLoraThreads;   // float4 of left a thread and stage
     static constexpr size_t stage_bytes = (size_t)SR * kPitch16;
     static constexpr size_t plane_bytes = (size_t)TERMS * SR * kPlane * 2;          // one of two buffers
-    static constexpr size_t scale_bytes = (size_t)SR * (CW / 32);                   // one of two buffers
+    static constexpr size_t scale_bytes = (size_t)SR * (CW / 32) * 2;               // one of two buffers
     static constexpr size_t work = kGradStages * stage_bytes + 2 * plane_bytes + 2 * scale_bytes + 2 * SR * 4;
     static constexpr size_t sums = sizeof(float) * (size_t)kLoraWarps * RP * kStride;
     static constexpr size_t smem = work > sums ? work : sums;
@@ -1124,8 +1129,8 @@ __device__ __forceinline__ void grad_body(const LoraGradArgs& p, const LoraGradS
     const int CS = (int)cluster_size(), crank = (int)cluster_rank();
     uint8_t* s_stage = smem;
     uint16_t* s_plane = reinterpret_cast<uint16_t*>(smem + kGradStages * S::stage_bytes);
-    uint8_t* s_scale = smem + kGradStages * S::stage_bytes + 2 * S::plane_bytes;
-    int* s_row = reinterpret_cast<int*>(s_scale + 2 * S::scale_bytes);
+    uint16_t* s_step = reinterpret_cast<uint16_t*>(smem + kGradStages * S::stage_bytes + 2 * S::plane_bytes);
+    int* s_row = reinterpret_cast<int*>(smem + kGradStages * S::stage_bytes + 2 * S::plane_bytes + 2 * S::scale_bytes);
     const uint32_t stage0 = smem_addr(s_stage), plane0 = smem_addr(s_plane);
 
     const int64_t lo = clamp_row(p.offsets[e], p.R), hi = clamp_row(p.offsets[e + 1], p.R);
@@ -1210,7 +1215,7 @@ __device__ __forceinline__ void grad_body(const LoraGradArgs& p, const LoraGradS
 #pragma unroll
             for (int q = 0; q < (SR * (CW / 32) + kLoraThreads - 1) / kLoraThreads; ++q) {
                 const int id = q * kLoraThreads + tid;
-                if (id < SR * (CW / 32)) s_scale[(i & 1) * S::scale_bytes + id] = (uint8_t)scale[q];
+                if (id < SR * (CW / 32)) s_step[(i & 1) * (S::scale_bytes / 2) + id] = (uint16_t)act8_step_bf16(scale[q]);
             }
         }
     };
@@ -1279,31 +1284,33 @@ __device__ __forceinline__ void grad_body(const LoraGradArgs& p, const LoraGradS
                         }
                 }
             } else {
-                // this lane's rows 2t, 2t+1, 2t+8, 2t+9, its CT columns from CT g on
-                uint32_t v[4][CT / 2];
+                uint32_t code_frag[CT][2];
+                // this lane's rows 2t, 2t+1 and 2t+8, 2t+9, its CT columns from CT g on; MMA tile c takes
+                // column c of them, a byte of either row of a pair, as two bf16 numbers
 #pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    const int row = r0 + 2 * t + (r & 1) + 8 * (r >> 1);
-                    const uint8_t* at = s_stage + (i % kGradStages) * S::stage_bytes + row * S::kPitch8 + wc * S::SC + CT * g;
-                    uint2 q;
-                    if constexpr (CT == 8) q = *reinterpret_cast<const uint2*>(at);
-                    else q = make_uint2(*reinterpret_cast<const uint32_t*>(at), 0u);
-                    const float step = act8_step(s_scale[(i & 1) * S::scale_bytes + row * (CW / 32) + (wc * S::SC + CT * g) / 32]);
-                    float f[8];
-                    act8_values(q, step, f);
+                for (int pair = 0; pair < 2; ++pair) {
+                    const int row = r0 + 2 * t + 8 * pair;
+                    const uint32_t at = x + (uint32_t)(row * S::kPitch8 + wc * S::SC + CT * g);
+                    uint32_t w[2][CT / 4];
+                    if constexpr (CT == 8) {
+                        const uint2 u = lds8(at), v = lds8(at + S::kPitch8);
+                        w[0][0] = u.x, w[0][1] = u.y, w[1][0] = v.x, w[1][1] = v.y;
+                    } else {
+                        w[0][0] = lds4(at), w[1][0] = lds4(at + S::kPitch8);
+                    }
+                    const uint16_t* st = s_step + (i & 1) * (S::scale_bytes / 2) + row * (CW / 32) + (wc * S::SC + CT * g) / 32;
+                    const uint32_t step = (uint32_t)st[0] | (uint32_t)st[CW / 32] << 16;
 #pragma unroll
-                    for (int w = 0; w < CT / 2; ++w) v[r][w] = pack_bf16x2(f[2 * w], f[2 * w + 1]);
+                    for (int c = 0; c < CT; ++c)
+                        code_frag[c][pair] = act8_pair(prmt(w[0][c / 4], w[1][c / 4], 0x0400u + 0x0101u * (c & 3)), step);
                 }
 #pragma unroll
-                for (int c = 0; c < CT; ++c) {
-                    const uint32_t sel = (c & 1) ? 0x7632u : 0x5410u;
-                    const uint32_t b0 = prmt(v[0][c / 2], v[1][c / 2], sel), b1 = prmt(v[2][c / 2], v[3][c / 2], sel);
+                for (int c = 0; c < CT; ++c)
 #pragma unroll
                     for (int m = 0; m < MT; ++m)
 #pragma unroll
                         for (int k = 0; k < TERMS; ++k)
-                            mma_bf16_16816(acc[m][c], a[m][k][0], a[m][k][1], a[m][k][2], a[m][k][3], b0, b1);
-                }
+                            mma_bf16_16816(acc[m][c], a[m][k][0], a[m][k][1], a[m][k][2], a[m][k][3], code_frag[c][0], code_frag[c][1]);
             }
         }
     }
@@ -1342,24 +1349,33 @@ __device__ __forceinline__ void grad_body(const LoraGradArgs& p, const LoraGradS
         cluster_arrive();
         cluster_wait();
     }
-    // the cluster's CTAs share the elements out
-    const int share = (CW * RP + CS - 1) / CS;
-    const int i1 = min((crank + 1) * share, CW * RP);
+    // the cluster's CTAs share the elements out, eight at a time along the gradient's contiguous
+    // axis: its columns (dA) or the rank (dB); C and r are multiples of 8
+    constexpr int kEights = CW * RP / 8;
+    const int share = (kEights + CS - 1) / CS;
+    const int i1 = min((crank + 1) * share, kEights);
     for (int i = crank * share + tid; i < i1; i += kLoraThreads) {
-        const int w = i / (RP * S::SC), q = i % (RP * S::SC);
-        // consecutive threads along the gradient's contiguous axis: its columns (dA) or the rank (dB)
-        const int j = d.transposed ? q % RP : q / S::SC, n = d.transposed ? q / RP : q % S::SC;
-        const int c = col0 + w * S::SC + n;
-        if (j >= p.r || c >= d.C) continue;
-        const float* at = s_red + (size_t)w * RP * S::kStride + j * S::kStride + n;
-        float v = 0.0f;
+        // dA: (rank, columns 8c..); dB: (column, ranks 8c..), the two halves of a column's ranks in turn
+        const int j = d.transposed ? 8 * (i % (RP / 8)) : i / (CW / 8), n = d.transposed ? i / (RP / 8) : 8 * (i % (CW / 8));
+        if (j >= p.r || col0 + n >= d.C) continue;
+        const float* at = s_red + (size_t)(n / S::SC) * RP * S::kStride + j * S::kStride + n % S::SC;
+        const int next = d.transposed ? S::kStride : 1;
+        float v[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) v[k] = CS > 1 ? 0.0f : at[k * next];
         if (CS > 1)
-            for (int k = 0; k < CS; ++k) v += ld_cluster(at, k);
-        else
-            v = *at;
-        const int64_t o = (int64_t)e * p.r * d.C + (d.transposed ? (int64_t)c * p.r + j : (int64_t)j * d.C + c);
-        if (TERMS == 3) reinterpret_cast<float*>(d.out)[o] = v;
-        else reinterpret_cast<uint16_t*>(d.out)[o] = f32_to_bf16_rne(v);
+            for (int q = 0; q < CS; ++q)
+#pragma unroll
+                for (int k = 0; k < 8; ++k) v[k] += ld_cluster(at + k * next, q);
+        const int64_t o = (int64_t)e * p.r * d.C + (d.transposed ? (int64_t)(col0 + n) * p.r + j : (int64_t)j * d.C + col0 + n);
+        if constexpr (TERMS == 3) {
+            float4* to = reinterpret_cast<float4*>(reinterpret_cast<float*>(d.out) + o);
+            to[0] = make_float4(v[0], v[1], v[2], v[3]);
+            to[1] = make_float4(v[4], v[5], v[6], v[7]);
+        } else {
+            *reinterpret_cast<uint4*>(reinterpret_cast<uint16_t*>(d.out) + o) =
+                make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
+        }
     }
     if (CS > 1) {                                        // a CTA's sums are read until here
         cluster_arrive();

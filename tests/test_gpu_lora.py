@@ -272,6 +272,23 @@ def test_parts_of_the_backward():
     assert none is None and torch.equal(dA3, dA) and torch.equal(dB3, dB)
 
 
+@pytest.mark.parametrize("r", [16, 72])
+def test_checkpoint_of_any_size_reads_as_its_values(r):
+    # every exponent bf16 has: the gradient from the codes is the gradient from their values, bit for bit
+    g = lib()
+    rng = np.random.default_rng(r)
+    T, K = 50, 288
+    x = rng.integers(0, 1 << 16, (T, K), dtype=np.uint16)
+    e = np.clip(rng.integers(0, 250, (T, K // 32, 1)) - rng.integers(0, 9, (T, K // 32, 32)), 0, 249).reshape(T, K)
+    x = torch.from_numpy(((x & 0x807F) | (e << 7).astype(np.uint16)).view(np.int16)).cuda().view(torch.bfloat16)
+    q = g.quantize_act8(x)
+    off = torch.tensor([0, 20, 20, T], device="cuda")
+    gh = torch.randn(T, r, device="cuda") * 1e-3
+    for dt in (torch.bfloat16, torch.float32):
+        assert torch.equal(g.lora_grad_a(gh, off, act8=q, grad_dtype=dt),
+                           g.lora_grad_a(gh, off, x=g.dequantize_act8(*q), grad_dtype=dt))
+
+
 def test_no_rows():
     g = lib()
     p = Problem([0, 0, 0], 16, 64, 32)
