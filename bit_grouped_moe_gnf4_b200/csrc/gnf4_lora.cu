@@ -109,13 +109,29 @@ __device__ __forceinline__ uint32_t cluster_size() {
 }
 __device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release;" ::: "memory"); }
 __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire;" ::: "memory"); }
-// a float of another CTA's shared memory, at the address that `local` has in this CTA's
-__device__ __forceinline__ float ld_cluster(const float* local, uint32_t rank) {
-    uint32_t a;
-    float v;
-    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_addr(local)), "r"(rank));
-    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(a) : "memory");
-    return v;
+// The sum over the cluster's CTAs of the four floats at `local` in their shared memory. All
+// loads are issued before the first sum: one by one they would cost a microsecond each.
+__device__ __forceinline__ float4 cluster_sum(const float* local, int size) {
+    constexpr int kMost = 8;
+    float4 v[kMost];
+#pragma unroll
+    for (int c = 0; c < kMost; ++c) {
+        v[c] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        if (c < size) {
+            uint32_t a;
+            asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_addr(local)), "r"(c));
+            asm volatile("ld.shared::cluster.v4.f32 {%0,%1,%2,%3}, [%4];"
+                         : "=f"(v[c].x), "=f"(v[c].y), "=f"(v[c].z), "=f"(v[c].w) : "r"(a));
+        }
+    }
+#pragma unroll
+    for (int c = 1; c < kMost; ++c) {
+        v[0].x += v[c].x;
+        v[0].y += v[c].y;
+        v[0].z += v[c].z;
+        v[0].w += v[c].w;
+    }
+    return v[0];
 }
 
 // rows of adapter e, kept inside [0, R] whatever the offsets hold
@@ -373,9 +389,11 @@ __global__ void __launch_bounds__(kLoraThreads, RowsShape<RP, MT>::kCtas) lora_r
             if (local < rows && j < p.r) {
                 const float* at = s_red + local * S::kRed + j;
                 if (have && CS > 1) {
-                    for (int c = 0; c < CS; ++c)
 #pragma unroll
-                        for (int k = 0; k < PER; ++k) v[k] += ld_cluster(at + k, c);
+                    for (int k = 0; k < PER; k += 4) {
+                        const float4 a = cluster_sum(at + k, CS);
+                        v[k] = a.x, v[k + 1] = a.y, v[k + 2] = a.z, v[k + 3] = a.w;
+                    }
                 } else if (have) {
 #pragma unroll
                     for (int k = 0; k < PER; k += 4) {
@@ -1345,28 +1363,31 @@ __device__ __forceinline__ void grad_body(const LoraGradArgs& p, const LoraGradS
         }
         __syncthreads();
     }
+    // the cluster's CTAs share the columns out and add up theirs, in place: no other CTA reads those
+    const int own = CW / CS, own0 = crank * own;
     if (CS > 1) {
         cluster_arrive();
         cluster_wait();
+        for (int i = tid; i < RP * own / 4; i += kLoraThreads) {
+            const int j = i / (own / 4), n = own0 + 4 * (i % (own / 4));
+            float* at = s_red + (size_t)(n / S::SC) * RP * S::kStride + j * S::kStride + n % S::SC;
+            *reinterpret_cast<float4*>(at) = cluster_sum(at, CS);
+        }
+        cluster_arrive();                                // a CTA's sums are read until here
+        __syncthreads();
     }
-    // the cluster's CTAs share the elements out, eight at a time along the gradient's contiguous
-    // axis: its columns (dA) or the rank (dB); C and r are multiples of 8
-    constexpr int kEights = CW * RP / 8;
-    const int share = (kEights + CS - 1) / CS;
-    const int i1 = min((crank + 1) * share, kEights);
-    for (int i = crank * share + tid; i < i1; i += kLoraThreads) {
-        // dA: (rank, columns 8c..); dB: (column, ranks 8c..), the two halves of a column's ranks in turn
-        const int j = d.transposed ? 8 * (i % (RP / 8)) : i / (CW / 8), n = d.transposed ? i / (RP / 8) : 8 * (i % (CW / 8));
+    // eight at a time along the gradient's contiguous axis: its columns (dA) or the rank (dB); C
+    // and r are multiples of 8
+    for (int i = tid; i < own * RP / 8; i += kLoraThreads) {
+        // dA: (rank, columns n..); dB: (column, ranks j..), the pieces of a column's ranks in turn
+        const int j = d.transposed ? 8 * (i % (RP / 8)) : i / (own / 8);
+        const int n = own0 + (d.transposed ? i / (RP / 8) : 8 * (i % (own / 8)));
         if (j >= p.r || col0 + n >= d.C) continue;
         const float* at = s_red + (size_t)(n / S::SC) * RP * S::kStride + j * S::kStride + n % S::SC;
         const int next = d.transposed ? S::kStride : 1;
         float v[8];
 #pragma unroll
-        for (int k = 0; k < 8; ++k) v[k] = CS > 1 ? 0.0f : at[k * next];
-        if (CS > 1)
-            for (int q = 0; q < CS; ++q)
-#pragma unroll
-                for (int k = 0; k < 8; ++k) v[k] += ld_cluster(at + k * next, q);
+        for (int k = 0; k < 8; ++k) v[k] = at[k * next];
         const int64_t o = (int64_t)e * p.r * d.C + (d.transposed ? (int64_t)(col0 + n) * p.r + j : (int64_t)j * d.C + col0 + n);
         if constexpr (TERMS == 3) {
             float4* to = reinterpret_cast<float4*>(reinterpret_cast<float*>(d.out) + o);
@@ -1377,10 +1398,7 @@ __device__ __forceinline__ void grad_body(const LoraGradArgs& p, const LoraGradS
                 make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
         }
     }
-    if (CS > 1) {                                        // a CTA's sums are read until here
-        cluster_arrive();
-        cluster_wait();
-    }
+    if (CS > 1) cluster_wait();
 }
 
 // CTAs (or clusters) of one adapter for one gradient; none for a gradient that is not asked for
