@@ -106,6 +106,7 @@ struct LoraGradArgs {
     const float* scaling;       // [L] or null
     int64_t R;
     int L, r;
+    int after_rows;             // a.left comes from the rows kernel launched just before on the stream
 };
 cudaError_t launch_lora_grads(const LoraGradArgs& a, bool f32, cudaStream_t s);
 cudaError_t launch_check_lora(const int64_t* offsets, int L, int64_t R, const int32_t* a, int64_t na, const int32_t* b,

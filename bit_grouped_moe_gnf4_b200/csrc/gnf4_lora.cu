@@ -134,6 +134,11 @@ __device__ __forceinline__ float4 cluster_sum(const float* local, int size) {
     return v[0];
 }
 
+// the grid behind this one may start where SMs are free (it waits for this one before it reads its results)
+__device__ __forceinline__ void let_next_grid_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+// the grid before this one (the rows kernel of the same call) may still run: wait for it
+__device__ __forceinline__ void wait_for_previous_grid() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
 // rows of adapter e, kept inside [0, R] whatever the offsets hold
 __device__ __forceinline__ int64_t clamp_row(int64_t v, int64_t R) { return v < 0 ? 0 : v > R ? R : v; }
 
@@ -252,6 +257,7 @@ __global__ void __launch_bounds__(kLoraThreads, RowsShape<RP, MT>::kCtas) lora_r
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int g = lane >> 2, t = lane & 3;
     const int CS = (int)cluster_size(), crank = (int)cluster_rank();
+    if (BWD) let_next_grid_start();
     find_tile<BM>(p.offsets, p.L, p.R, (int)(blockIdx.x / CS), &s_tile, s_warp);
     const int rows = s_tile.rows, e = s_tile.e;
     const int64_t row0 = s_tile.row0;
@@ -637,6 +643,7 @@ __global__ void __launch_bounds__(StreamShape<RP>::kThreads, StreamShape<RP>::kC
         s_abort = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
+    if (BWD) let_next_grid_start();
     // the adapters' tiles, a run of neighbouring adapters a thread
     {
         const int per = (p.L + S::kThreads - 1) / S::kThreads;
@@ -1197,7 +1204,7 @@ __device__ __forceinline__ void grad_body(const LoraGradArgs& p, const LoraGradS
             fac[q] = scal;
             if (id < SR * RP / 4 && local < rows && j < p.r) {
                 const int64_t r = lo + local;
-                left[q] = __ldg(reinterpret_cast<const float4*>(d.left + r * p.r + j));
+                left[q] = *reinterpret_cast<const float4*>(d.left + r * p.r + j);
                 if (d.factor && p.weight) fac[q] *= __ldg(p.weight + r);
             }
         }
@@ -1252,15 +1259,16 @@ __device__ __forceinline__ void grad_body(const LoraGradArgs& p, const LoraGradS
         s_row[tid] = source_row(first(0) + tid);
         s_row[SR + tid] = source_row(first(1) + tid);
     }
-    fetch(0);
     __syncthreads();
     if (stages > 0) issue(0);
     copy_commit();
     if (stages > 1) issue(1);
     copy_commit();
+    int next_row = tid < SR ? source_row(first(2) + tid) : -1;
+    if (!d.factor) wait_for_previous_grid();            // dA's left comes from the rows kernel; the copies do not
+    fetch(0);
     place(0);
     fetch(1);
-    int next_row = tid < SR ? source_row(first(2) + tid) : -1;
     __syncthreads();                                    // s_row has been read
     if (tid < SR) s_row[tid] = next_row;                // stage 2's
     next_row = tid < SR ? source_row(first(3) + tid) : -1;
@@ -1399,6 +1407,7 @@ __device__ __forceinline__ void grad_body(const LoraGradArgs& p, const LoraGradS
         }
     }
     if (CS > 1) cluster_wait();
+    if (tid == 0) wait_for_previous_grid();              // whoever waits for this grid waits for that one too
 }
 
 // CTAs (or clusters) of one adapter for one gradient; none for a gradient that is not asked for
@@ -1412,9 +1421,9 @@ __global__ void __launch_bounds__(kLoraThreads, RP <= 32 && WR == 1 ? 2 : 1) lor
     constexpr int CW = GradShape<RP, WR, TERMS>::CW;
     const int item = (int)(blockIdx.x / cluster_size());
     const int na = grad_items(p.a, CW), nb = grad_items(p.b, CW);
-    const int e = item / (na + nb), i = item % (na + nb);
-    if (i < na) grad_body<RP, WR, TERMS, Q8>(p, p.a, e, i * CW, smem);
-    else grad_body<RP, WR, TERMS, false>(p, p.b, e, (i - na) * CW, smem);
+    // dB's items come first: they need nothing of the rows kernel and fill the SMs that it leaves
+    if (item < nb * p.L) grad_body<RP, WR, TERMS, false>(p, p.b, item / nb, item % nb * CW, smem);
+    else grad_body<RP, WR, TERMS, Q8>(p, p.a, (item - nb * p.L) / na, (item - nb * p.L) % na * CW, smem);
 }
 
 template <int RP, int WR, int TERMS, bool Q8>
@@ -1435,13 +1444,15 @@ cudaError_t launch_grads_t(const LoraGradArgs& a, int cs, cudaStream_t s) {
     cfg.blockDim = dim3(kLoraThreads);
     cfg.dynamicSmemBytes = S::smem;
     cfg.stream = s;
-    cudaLaunchAttribute at[1];
+    cudaLaunchAttribute at[2];
     at[0].id = cudaLaunchAttributeClusterDimension;
     at[0].val.clusterDim.x = (unsigned)cs;
     at[0].val.clusterDim.y = 1;
     at[0].val.clusterDim.z = 1;
+    at[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = at;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = a.after_rows ? 2 : 1;
     return cudaLaunchKernelEx(&cfg, lora_grads_kernel<RP, WR, TERMS, Q8>, a);
 }
 
