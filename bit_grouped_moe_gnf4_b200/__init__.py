@@ -17,11 +17,13 @@ __all__ = list(_API + _LIB)
 
 def __getattr__(name):
     # load libgnf4.so only when the binding is used, so that the build script
-    # (a submodule of this package) can run before the library exists
+    # (a submodule of this package) can run before the library exists; a name that has been
+    # looked up becomes an ordinary attribute
     if name in _API:
-        from . import api
-        return getattr(api, name)
-    if name in _LIB:
-        from . import _lib
-        return getattr(_lib, name)
-    raise AttributeError(name)
+        from . import api as module
+    elif name in _LIB:
+        from . import _lib as module
+    else:
+        raise AttributeError(name)
+    globals()[name] = getattr(module, name)
+    return globals()[name]

@@ -326,7 +326,7 @@ def _act8(act8, K: int, name: str):
     codes, scales = act8
     _need(codes, torch.int8, f"{name} codes")
     _need(scales, torch.uint8, f"{name} scales")
-    if codes.dim() != 2 or codes.shape[1] != K or tuple(scales.shape) != (codes.shape[0], K // 32):
+    if codes.dim() != 2 or codes.shape[1] != K or scales.shape != (codes.shape[0], K // 32):
         raise ValueError(f"{name} must be codes [rows, {K}] and scales [rows, {K // 32}], got "
                          f"{list(codes.shape)} and {list(scales.shape)}")
     return codes, scales
@@ -338,8 +338,10 @@ def quantize_act8(x: torch.Tensor, codes: Optional[torch.Tensor] = None, scales:
     ``[..., K//32]``), one e8m0 scale per 32 elements (include/gnf4.h)."""
     _need(x, torch.bfloat16, "x")
     K = x.shape[-1]
+    if codes is None:
+        codes = torch.empty_like(x, dtype=torch.int8)
     codes = _shaped(codes, x.shape, torch.int8, "codes", x)
-    scales = _shaped(scales, tuple(x.shape[:-1]) + (K // 32,), torch.uint8, "scales", x)
+    scales = _shaped(scales, (*x.shape[:-1], K // 32), torch.uint8, "scales", x)
     check(lib.gnf4_quantize_act8(_ptr(x), x.numel() // K if K else 0, K, _ptr(codes), _ptr(scales), _stream(stream)),
           "gnf4_quantize_act8")
     return codes, scales
@@ -351,8 +353,10 @@ def dequantize_act8(codes: torch.Tensor, scales: torch.Tensor, out: Optional[tor
     _need(codes, torch.int8, "codes")
     K = codes.shape[-1]
     _need(scales, torch.uint8, "scales")
-    if tuple(scales.shape) != tuple(codes.shape[:-1]) + (K // 32,):
+    if scales.shape != (*codes.shape[:-1], K // 32):
         raise ValueError(f"scales must be [..., {K // 32}] beside codes {list(codes.shape)}, got {list(scales.shape)}")
+    if out is None:
+        out = torch.empty_like(codes, dtype=torch.bfloat16)
     out = _shaped(out, codes.shape, torch.bfloat16, "out", codes)
     check(lib.gnf4_dequantize_act8(_ptr(codes), _ptr(scales), codes.numel() // K if K else 0, K, _ptr(out),
                                    _stream(stream)), "gnf4_dequantize_act8")
@@ -368,6 +372,8 @@ def swiglu_act8(gate_up: torch.Tensor, out: Optional[torch.Tensor] = None, codes
         raise ValueError(f"gate_up must be [R, 2I], got {tuple(gate_up.shape)}")
     R, I = gate_up.shape[0], gate_up.shape[1] // 2
     out = _shaped(out, (R, I), torch.bfloat16, "out", gate_up)
+    if codes is None:
+        codes = torch.empty_like(gate_up, dtype=torch.int8)
     codes = _shaped(codes, (R, 2 * I), torch.int8, "codes", gate_up)
     scales = _shaped(scales, (R, 2 * I // 32), torch.uint8, "scales", gate_up)
     check(lib.gnf4_swiglu_act8(_ptr(gate_up), R, I, _ptr(out), _ptr(codes), _ptr(scales), _stream(stream)),
@@ -403,28 +409,39 @@ def swiglu_backward(grad_out: torch.Tensor, gate_up: Optional[torch.Tensor] = No
     return out if act is None else (out, act)
 
 
-def _lora_common(A, B, adapter_offsets, row_token, row_weight, rows, scaling, R, dtype):
+def _lora_common(A, B, adapter_offsets, row_token, row_weight, name, rows, scaling, R, dtype):
     _need(A, dtype, "A")
     _need(B, dtype, "B")
-    if A.dim() != 3 or B.dim() != 3 or A.shape[0] != B.shape[0] or A.shape[1] != B.shape[2]:
+    try:
+        (L, r, K), (L2, N, r2) = A.shape, B.shape
+    except ValueError:
+        L2 = None
+    if L2 is None or L != L2 or r != r2:
         raise ValueError(f"A must be [L, r, K] and B [L, N, r], got {list(A.shape)} and {list(B.shape)}")
-    L, r, K = A.shape
     _need(adapter_offsets, torch.int64, "adapter_offsets")
     if adapter_offsets.numel() != L + 1:
         raise ValueError(f"adapter_offsets must hold L + 1 = {L + 1} entries, got {adapter_offsets.numel()}")
-    arrays = (("row_token", row_token, torch.int32), ("row_weight", row_weight, torch.float32), rows)
-    for name, t, dt in arrays:
-        if t is not None:
-            _need(t, dt, name)
-            if R is None:
-                R = t.numel()
-            if t.numel() < R:
-                raise ValueError(f"{name} must hold R = {R} entries, got {t.numel()}")
+    if row_token is not None:
+        R = _row_array(row_token, torch.int32, "row_token", R)
+    if row_weight is not None:
+        R = _row_array(row_weight, torch.float32, "row_weight", R)
+    if rows is not None:
+        R = _row_array(rows, torch.int32, name, R)
     if scaling is not None:
         _need(scaling, torch.float32, "scaling")
         if scaling.numel() != L:
             raise ValueError(f"scaling must hold L = {L} entries, got {scaling.numel()}")
-    return L, r, K, B.shape[1], R
+    return L, r, K, N, R
+
+
+def _row_array(t, dtype, name, R):
+    _need(t, dtype, name)
+    n = t.numel()
+    if R is None:
+        return n
+    if n < R:
+        raise ValueError(f"{name} must hold R = {R} entries, got {n}")
+    return R
 
 
 def _lora_x(x, act8, K: int):
@@ -454,27 +471,29 @@ def lora_apply(base: Optional[torch.Tensor], x: torch.Tensor, A: torch.Tensor, B
     if x.dtype not in (torch.bfloat16, torch.float16):
         raise TypeError(f"x must be torch.bfloat16 or torch.float16, got {x.dtype}")
     _need(x, x.dtype, "x")
-    L, r, K, N, R = _lora_common(A, B, adapter_offsets, row_token, row_weight, ("row_dest", row_dest, torch.int32),
-                                 scaling, R, x.dtype)
+    L, r, K, N, R = _lora_common(A, B, adapter_offsets, row_token, row_weight, "row_dest", row_dest, scaling, R, x.dtype)
     if x.dim() != 2 or x.shape[1] != K:
         raise ValueError(f"x must be [T_in, K = {K}], got {list(x.shape)}")
+    T_in = x.shape[0]
     if R is None:
-        R = x.shape[0]
+        R = T_in
     if base is None and out is None:
         raise ValueError("give base, or out (then the adapters' product alone is written there)")
     if out is None:
         out = base
-    for name, t in (("base", base), ("out", out)):
-        if t is not None:
-            _need(t, x.dtype, name)
-            if t.dim() != 2 or t.shape != out.shape or t.shape[1] != N:
-                raise ValueError(f"{name} must be [T_out, N = {N}] (base and out alike), got {list(t.shape)}")
+    _need(out, x.dtype, "out")
+    if out.dim() != 2 or out.shape[1] != N:
+        raise ValueError(f"out must be [T_out, N = {N}], got {list(out.shape)}")
+    if base is not None and base is not out:
+        _need(base, x.dtype, "base")
+        if base.shape != out.shape:
+            raise ValueError(f"base and out must be alike, got {list(base.shape)} and {list(out.shape)}")
     if h is not None:
         h = _shaped(h, (R, r), torch.float32, "h", x)
     xdt = _lib.GNF4_DTYPE_F16 if x.dtype == torch.float16 else _lib.GNF4_DTYPE_BF16
     check(lib.gnf4_lora_apply(_ptr(base), _ptr(x), xdt, _ptr(A), _ptr(B), _ptr(adapter_offsets), _ptr(row_token),
-                              _ptr(row_weight), _ptr(row_dest), _ptr(scaling), L, r, N, K, R, x.shape[0],
-                              out.shape[0], _ptr(out), _ptr(h), flags, _stream(stream)), "gnf4_lora_apply")
+                              _ptr(row_weight), _ptr(row_dest), _ptr(scaling), L, r, N, K, R, T_in, out.shape[0],
+                              _ptr(out), _ptr(h), flags, _stream(stream)), "gnf4_lora_apply")
     return out
 
 
@@ -492,8 +511,8 @@ def lora_backward(grad_out: torch.Tensor, h: torch.Tensor, A: torch.Tensor, B: t
     scales)`` its checkpoint; with neither dA is None, and ``lora_grad_a`` gives it from ``grad_h``; ``h`` what the forward wrote; ``row_src`` its ``row_dest``. ``grad_h``
     (fp32 ``[R, r]``) is the call's own buffer; it has to be given together with ``stream``."""
     _need(grad_out, torch.bfloat16, "grad_out")
-    L, r, K, N, R = _lora_common(A, B, adapter_offsets, row_token, row_weight, ("row_src", row_src, torch.int32),
-                                 scaling, R, torch.bfloat16)
+    L, r, K, N, R = _lora_common(A, B, adapter_offsets, row_token, row_weight, "row_src", row_src, scaling, R,
+                                 torch.bfloat16)
     if grad_dtype not in (torch.bfloat16, torch.float32):
         raise TypeError(f"grad_dtype must be torch.bfloat16 or torch.float32, got {grad_dtype}")
     if grad_out.dim() != 2 or grad_out.shape[1] != N:
@@ -516,11 +535,11 @@ def lora_backward(grad_out: torch.Tensor, h: torch.Tensor, A: torch.Tensor, B: t
         want_dx = True
         _shaped(dx_base, (R, K), torch.bfloat16, "dx_base", grad_out)
     if want_dx or dx is not None:
-        dx = _shaped(dx, (R, K), torch.bfloat16, "dx", grad_out)
+        dx = _shaped(dx, (R, K), torch.bfloat16, "dx", grad_out if dx_base is None else dx_base)
     if x is not None or act8 is not None:
-        dA = _shaped(dA, (L, r, K), grad_dtype, "dA", grad_out)
-    dB = _shaped(dB, (L, N, r), grad_dtype, "dB", grad_out)
-    grad_h = _shaped(grad_h, (R, r), torch.float32, "grad_h", grad_out)
+        dA = _shaped(dA, (L, r, K), grad_dtype, "dA", A)
+    dB = _shaped(dB, (L, N, r), grad_dtype, "dB", B)
+    grad_h = _shaped(grad_h, (R, r), torch.float32, "grad_h", h)
     gdt = _lib.GNF4_DTYPE_F32 if grad_dtype == torch.float32 else _lib.GNF4_DTYPE_BF16
     check(lib.gnf4_lora_backward(_ptr(grad_out), _ptr(x), _ptr(codes), _ptr(scales), _ptr(h), _ptr(A), _ptr(B),
                                  _ptr(adapter_offsets), _ptr(row_token), _ptr(row_weight), _ptr(row_src),

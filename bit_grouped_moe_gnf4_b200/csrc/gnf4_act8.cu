@@ -10,7 +10,7 @@
 //
 // All four kernels stream 16-byte vectors of 8 bf16 (8 codes are 8 bytes); four
 // neighbouring lanes hold one block of 32, so a block's scale is two shuffles. They are
-// bound by HBM: the arithmetic is about 6 instructions an element for the codes and 15 for
+// bound by HBM: the arithmetic is about 4 instructions an element for the codes and 15 for
 // the SwiGLU's gradients.
 #include <cstdint>
 #include <cuda_runtime.h>
@@ -46,36 +46,60 @@ __device__ __forceinline__ uint32_t block_scale(const uint4& v) {
     return m >> 7;
 }
 
-// a value times 2^(133-s), rounded to nearest even and clamped, in the low byte: adding
-// 1.5 * 2^23 leaves the rounded integer in the low mantissa bits (two's complement)
-__device__ __forceinline__ uint32_t code_of(float scaled) {
-    return __float_as_uint(fminf(fmaxf(scaled, -127.0f), 127.0f) + 12582912.0f);
+// four codes in the low bytes of c; 128 and -128 are one pattern there and become +-127
+__device__ __forceinline__ uint32_t pack_codes(const uint32_t* c) {
+    uint32_t w = prmt(prmt(c[0], c[1], 0x0040u), prmt(c[2], c[3], 0x0040u), 0x5410u);
+    const uint32_t y = w ^ 0x80808080u;
+    if ((y - 0x01010101u) & ~y & 0x80808080u) {          // a byte is 0x80: the block's largest value rounded up
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if ((c[i] & 0xFFu) == 0x80u) w ^= ((int32_t)(c[i] << 9) < 0 ? 0xFFu : 0x01u) << (8 * i);
+    }
+    return w;
 }
 
+// A code is the value times 2^(133-s), at most 127.5 of either sign, rounded to nearest even:
+// the fused multiply-add onto 1.5 * 2^23 leaves the integer in the low mantissa bits (two's
+// complement, bit 22 clear for a negative one), with one rounding.
 __device__ __forceinline__ uint2 encode8(const uint4& v, uint32_t s) {
     if (s == 255u) return make_uint2(0u, 0u);
+    uint32_t c[8];
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
     // 2^(133-s) is an fp32 number for s >= 6; below that in two exact steps
     const float up = __uint_as_float((260u - max(s, 6u)) << 23);
-    const float more = __uint_as_float((127u + max(s, 6u) - s) << 23);
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-    uint32_t c[8];
+    const float more = s < 6u ? __uint_as_float((133u - s) << 23) : 1.0f;
+    if (s < 6u) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        c[2 * i] = code_of(lo_f(w[i]) * more * up);
-        c[2 * i + 1] = code_of(hi_f(w[i]) * more * up);
+        for (int i = 0; i < 4; ++i) {
+            c[2 * i] = __float_as_uint(fmaf(lo_f(w[i]) * more, up, 12582912.0f));
+            c[2 * i + 1] = __float_as_uint(fmaf(hi_f(w[i]) * more, up, 12582912.0f));
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            c[2 * i] = __float_as_uint(fmaf(lo_f(w[i]), up, 12582912.0f));
+            c[2 * i + 1] = __float_as_uint(fmaf(hi_f(w[i]), up, 12582912.0f));
+        }
     }
-    uint2 o;
-    o.x = prmt(prmt(c[0], c[1], 0x0040u), prmt(c[2], c[3], 0x0040u), 0x5410u);
-    o.y = prmt(prmt(c[4], c[5], 0x0040u), prmt(c[6], c[7], 0x0040u), 0x5410u);
-    return o;
+    return make_uint2(pack_codes(c), pack_codes(c + 4));
 }
 
 __device__ __forceinline__ uint4 decode8(const uint2& q, uint32_t s) {
-    float f[8];
-    act8_values(q, act8_step(s), f);
-    return make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]),
-                      pack_bf16x2(f[6], f[7]));
+    const uint32_t step = act8_step_bf16(s) * 0x00010001u;
+    return make_uint4(act8_pair(prmt(q.x, 0u, 0x0100u), step), act8_pair(prmt(q.x, 0u, 0x0302u), step),
+                      act8_pair(prmt(q.y, 0u, 0x0100u), step), act8_pair(prmt(q.y, 0u, 0x0302u), step));
 }
+
+// r = i / d for the 32-bit walks: a multiplication and two shifts (the round-up method of Granlund
+// and Montgomery, 1994)
+struct Divider {
+    uint32_t d, m, s;
+    __device__ uint32_t operator()(uint32_t i) const {
+        const uint32_t t = __umulhi(m, i);
+        return (t + ((i - t) >> 1)) >> s;
+    }
+    __device__ int64_t operator()(int64_t i) const { return i / (int64_t)d; }
+};
 
 // total: 16-byte vectors; a multiple of 4, so the four lanes of a block are all in range or all out
 __global__ void __launch_bounds__(kActThreads) quantize_act8_kernel(const uint4* __restrict__ x, uint2* __restrict__ codes,
@@ -133,7 +157,8 @@ __device__ __forceinline__ uint32_t silu_word(uint32_t g, uint32_t u) {
 template <typename IDX>
 __global__ void __launch_bounds__(kActThreads) swiglu_act8_kernel(const uint4* __restrict__ h, uint4* __restrict__ out,
                                                                   uint2* __restrict__ codes,
-                                                                  uint8_t* __restrict__ scales, IDX I8, IDX total) {
+                                                                  uint8_t* __restrict__ scales, Divider by, IDX total) {
+    const IDX I8 = (IDX)by.d;
     const IDX stride = (IDX)gridDim.x * (kActThreads * kSwigluActVecs);
     for (IDX b = (IDX)blockIdx.x * (kActThreads * kSwigluActVecs); b < total; b += stride) {
         uint4 g[kSwigluActVecs], u[kSwigluActVecs];
@@ -144,7 +169,7 @@ __global__ void __launch_bounds__(kActThreads) swiglu_act8_kernel(const uint4* _
             g[j] = u[j] = make_uint4(0u, 0u, 0u, 0u);
             at[j] = 0;
             if (i < total) {
-                const IDX r = i / I8;
+                const IDX r = by(i);
                 at[j] = (int64_t)i + (int64_t)r * I8;      // r * 2 I8 + (i - r I8)
                 g[j] = __ldg(h + at[j]);
                 u[j] = __ldg(h + at[j] + I8);
@@ -194,7 +219,8 @@ __global__ void __launch_bounds__(kActThreads) swiglu_backward_kernel(const uint
                                                                       const uint2* __restrict__ codes,
                                                                       const uint8_t* __restrict__ scales,
                                                                       uint4* __restrict__ dh, uint4* __restrict__ again,
-                                                                      IDX I8, IDX total) {
+                                                                      Divider by, IDX total) {
+    const IDX I8 = (IDX)by.d;
     const IDX stride = (IDX)gridDim.x * (kActThreads * kSwigluActVecs);
     for (IDX base = (IDX)blockIdx.x * (kActThreads * kSwigluActVecs) + threadIdx.x; base < total; base += stride) {
         uint4 g[kSwigluActVecs], u[kSwigluActVecs], dv[kSwigluActVecs];
@@ -205,7 +231,7 @@ __global__ void __launch_bounds__(kActThreads) swiglu_backward_kernel(const uint
         for (int j = 0; j < kSwigluActVecs; ++j) {
             const IDX i = base + (IDX)j * kActThreads;
             if (i < total) {
-                const IDX r = i / I8;
+                const IDX r = by(i);
                 at[j] = (int64_t)i + (int64_t)r * I8;
                 dv[j] = __ldg(d + i);
                 if (Q8) {
@@ -249,9 +275,21 @@ int act_grid(int64_t total, int per_thread) {
     return (int)(want < cap ? want : cap);
 }
 
+// I8 vectors a row, 1 < I8 < 2^31 (1 has no shift of its own: the 64-bit walk takes it)
+Divider divider(int64_t I8) {
+    Divider v{(uint32_t)I8, 0u, 0u};
+    int l = 0;
+    while ((1ll << l) < I8) ++l;
+    if (l > 0) {
+        v.m = (uint32_t)(((1ull << 32) * ((1ull << l) - (uint64_t)I8)) / (uint64_t)I8 + 1);
+        v.s = (uint32_t)(l - 1);
+    }
+    return v;
+}
+
 // whether every index a 32-bit walk over `total` vectors forms fits in 32 bits
-bool fits_u32(int64_t total, int grid, int per_thread) {
-    return total <= (int64_t)UINT32_MAX - 2 * (int64_t)grid * kActThreads * per_thread;
+bool fits_u32(int64_t total, int grid, int per_thread, int64_t I8) {
+    return total <= (int64_t)UINT32_MAX - 2 * (int64_t)grid * kActThreads * per_thread && I8 > 1;
 }
 
 }  // namespace
@@ -277,10 +315,10 @@ cudaError_t launch_swiglu_act8(const void* gate_up, int64_t R, int64_t I, void* 
     const uint4* h = reinterpret_cast<const uint4*>(gate_up);
     uint4* o = reinterpret_cast<uint4*>(out);
     uint2* q = reinterpret_cast<uint2*>(codes);
-    if (fits_u32(total, grid, kSwigluActVecs))
-        swiglu_act8_kernel<uint32_t><<<grid, kActThreads, 0, s>>>(h, o, q, scales, (uint32_t)I8, (uint32_t)total);
+    if (fits_u32(total, grid, kSwigluActVecs, I8))
+        swiglu_act8_kernel<uint32_t><<<grid, kActThreads, 0, s>>>(h, o, q, scales, divider(I8), (uint32_t)total);
     else
-        swiglu_act8_kernel<int64_t><<<grid, kActThreads, 0, s>>>(h, o, q, scales, I8, total);
+        swiglu_act8_kernel<int64_t><<<grid, kActThreads, 0, s>>>(h, o, q, scales, divider(I8), total);
     return cudaGetLastError();
 }
 
@@ -293,15 +331,15 @@ cudaError_t launch_swiglu_backward(const void* d_out, const void* gate_up, const
     const uint2* q = reinterpret_cast<const uint2*>(codes);
     uint4* dh = reinterpret_cast<uint4*>(d_gate_up);
     uint4* a = reinterpret_cast<uint4*>(again);
-    const bool small = fits_u32(total, grid, kSwigluActVecs);
+    const bool small = fits_u32(total, grid, kSwigluActVecs, I8);
     if (gate_up && small)
-        swiglu_backward_kernel<uint32_t, false><<<grid, kActThreads, 0, s>>>(d, h, q, scales, dh, a, (uint32_t)I8, (uint32_t)total);
+        swiglu_backward_kernel<uint32_t, false><<<grid, kActThreads, 0, s>>>(d, h, q, scales, dh, a, divider(I8), (uint32_t)total);
     else if (gate_up)
-        swiglu_backward_kernel<int64_t, false><<<grid, kActThreads, 0, s>>>(d, h, q, scales, dh, a, I8, total);
+        swiglu_backward_kernel<int64_t, false><<<grid, kActThreads, 0, s>>>(d, h, q, scales, dh, a, divider(I8), total);
     else if (small)
-        swiglu_backward_kernel<uint32_t, true><<<grid, kActThreads, 0, s>>>(d, h, q, scales, dh, a, (uint32_t)I8, (uint32_t)total);
+        swiglu_backward_kernel<uint32_t, true><<<grid, kActThreads, 0, s>>>(d, h, q, scales, dh, a, divider(I8), (uint32_t)total);
     else
-        swiglu_backward_kernel<int64_t, true><<<grid, kActThreads, 0, s>>>(d, h, q, scales, dh, a, I8, total);
+        swiglu_backward_kernel<int64_t, true><<<grid, kActThreads, 0, s>>>(d, h, q, scales, dh, a, divider(I8), total);
     return cudaGetLastError();
 }
 

@@ -41,20 +41,22 @@ static gnf4_status cuda_fail(cudaError_t e, const char* what) {
 
 // device (or managed) memory of the current device; managed memory is accepted on
 // any device, since the GPU reaches it through page migration
-static bool is_device_ptr(const void* p) {
+static bool is_device_ptr(const void* p, int dev) {
     cudaPointerAttributes attr;
     if (cudaPointerGetAttributes(&attr, p) != cudaSuccess) {
         cudaGetLastError();
         return false;
     }
     if (attr.type == cudaMemoryTypeManaged) return true;
-    if (attr.type != cudaMemoryTypeDevice) return false;
+    return attr.type == cudaMemoryTypeDevice && attr.device == dev;
+}
+static bool is_device_ptr(const void* p) {
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) {
         cudaGetLastError();
         return false;
     }
-    return attr.device == dev;
+    return is_device_ptr(p, dev);
 }
 
 static bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
@@ -377,8 +379,10 @@ static bool aligned8(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 7
 
 // every buffer that is given (the last step of a check: alignment is refused before)
 static gnf4_status check_device(std::initializer_list<const void*> ptrs) {
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) cudaGetLastError();
     for (const void* q : ptrs)
-        if (q && !is_device_ptr(q))
+        if (q && !is_device_ptr(q, dev))
             return fail(GNF4_ERR_INVALID_ARG, "every buffer must be device memory of the current device");
     return GNF4_OK;
 }
@@ -401,7 +405,8 @@ static gnf4_status check_act8_sizes(int64_t rows, int64_t K) {
 static gnf4_status check_swiglu_sizes(int64_t R, int64_t I, int64_t imul) {
     if (R < 0 || I < 1) return fail(GNF4_ERR_INVALID_ARG, "sizes must be R >= 0 and I >= 1");
     if (I % imul) return fail(GNF4_ERR_UNSUPPORTED_SHAPE, "I must be a multiple of %lld", (long long)imul);
-    if (R > INT64_MAX / 4 / I) return fail(GNF4_ERR_UNSUPPORTED_SHAPE, "R * 2I must fit in int64");
+    if (I > (1 << 30) || R > INT64_MAX / 4 / I)
+        return fail(GNF4_ERR_UNSUPPORTED_SHAPE, "I must be at most 2^30 and R * 2I fit in int64");
     return GNF4_OK;
 }
 
