@@ -38,6 +38,7 @@ namespace gnf4 {
 namespace {
 
 constexpr int kLoraThreads = 256;
+constexpr size_t kMaxSmem = 227 * 1024 - 512;      // dynamic shared memory of a CTA beside its static part
 constexpr int kLoraWarps = kLoraThreads / 32;
 
 __device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
@@ -579,20 +580,19 @@ __global__ void __launch_bounds__(kLoraThreads, RowsShape<RP, MT>::kCtas) lora_r
 // warps to meet for the sums. All fragments come out of shared memory by ldmatrix.
 __device__ unsigned g_lora_err;               // set when a wait of the stream gives up
 
-template <int RP>
+template <int RP, int ROWS>
 struct StreamShape {
-    static constexpr int BM = 32, MT = 2, NT = RP / 8, KS = RP / 16;
+    static constexpr int BM = ROWS, MT = BM / 16, NT = RP / 8, KS = RP / 16;
     static constexpr int CW = 32 * kLoraWarps;                       // columns of a stage
-    static constexpr int kCtas = RP == 16 ? 2 : 1;                   // on an SM
-    static constexpr int kProducers = RP == 16 ? 64 : 128;           // threads; about 12 copies each a stage
+    static constexpr int kProducers = 128;                           // threads
     static constexpr int kThreads = kLoraThreads + kProducers;
-    static constexpr int kStages = RP == 32 ? 4 : 3;
+    static constexpr int kStages = RP == 16 ? (BM == 32 ? 6 : 4) : RP == 32 && BM == 32 ? 4 : 3;
     static constexpr int kRow = 2 * CW + 16;                         // bytes a row of CW columns
     static constexpr int kRank = RP == 16 ? 32 : 2 * RP + 16;        // bytes a row of the rank
     static constexpr int kFactor = CW * kRank > RP * kRow ? CW * kRank : RP * kRow;
     static constexpr int kStage = BM * kRow + kFactor;
     static constexpr int kRed = RP + 8;                              // floats a row
-    static constexpr int kSums = RP <= 32 ? 8 : 4;                   // warps' partial sums that are kept apart
+    static constexpr int kSums = RP <= 32 && BM == 32 ? 8 : 4;                   // warps' partial sums that are kept apart
     // Tiles whose row indices are kept: when the producers begin a tile they have issued all of
     // the ones before it, of at least two stages each, and all but kStages of those are released
     static constexpr int kTiles = 4;
@@ -617,9 +617,9 @@ __device__ __forceinline__ void copy_arrive(uint32_t bar) {
     asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
 }
 
-template <int RP, bool BWD, bool F16>
-__global__ void __launch_bounds__(StreamShape<RP>::kThreads, StreamShape<RP>::kCtas) lora_stream_kernel(const LoraRowsArgs p) {
-    using S = StreamShape<RP>;
+template <int RP, int ROWS, bool BWD, bool F16>
+__global__ void __launch_bounds__(StreamShape<RP, ROWS>::kThreads, 1) lora_stream_kernel(const LoraRowsArgs p) {
+    using S = StreamShape<RP, ROWS>;
     constexpr int BM = S::BM, MT = S::MT, NT = S::NT, KS = S::KS, CW = S::CW, NS = S::kStages, NP = S::kProducers;
     constexpr int kPlane = 2 * RP + 16;                              // bytes a row of h's terms
     extern __shared__ __align__(16) uint8_t smem[];
@@ -688,8 +688,8 @@ __global__ void __launch_bounds__(StreamShape<RP>::kThreads, StreamShape<RP>::kC
         // ------------------------------------------------------------ producers
         const int ptid = tid - kLoraThreads;
         int e = 0, row0 = 0, rows = 0;
-        // The tile's adapter and rows, and the row index that this thread keeps for the tile: 32
-        // sources and 32 destinations over the first 64 producers
+        // the tile's adapter and rows, and the row index that this thread keeps for the tile: its
+        // sources and then its destinations over the producers
         auto look_up = [&](int tile) -> int {
             if (tile >= tiles) return -1;
             int lo = 0, hi = p.L - 1;                                // the last adapter whose first tile <= tile
@@ -820,16 +820,18 @@ __global__ void __launch_bounds__(StreamShape<RP>::kThreads, StreamShape<RP>::kC
     const int by_n = (lane & 7) + 8 * (lane >> 4), by_k = (lane >> 3) & 1;
     const int k0 = 32 * warp;                                        // this warp's columns of every stage
     const uint32_t rows_frag = ring + by_row * S::kRow + 2 * k0 + by_col;
-    // in the second product a warp has 16 of the rows and 64 of the columns: whole 128-byte lines
-    const int wm = warp & 1, n0 = 64 * (warp >> 1);
+    // in the second product a warp has 16 of the rows and 64 or 128 of the columns: whole 128-byte lines
+    constexpr int SUB = MT;                                          // in pieces of 32
+    const int wm = warp % MT, n0 = 32 * SUB * (warp / MT);
+    constexpr int TPR = kLoraThreads / BM;                           // threads that finish a row of sums
     const uint32_t plane0 = smem_addr(s_plane) + (16 * wm + by_row) * kPlane + by_col;
     int buf = 0;
     for (int tile = blockIdx.x; tile < tiles; tile += gridDim.x, buf = (buf + 1) % S::kTiles) {
         const int* info = s_info + S::kInfo * buf;
         wait_stage();                                                // the tile's info is there with its first stage
         const int e = gone ? 0 : info[2 * BM], row0 = gone ? 0 : info[2 * BM + 1], rows = gone ? 0 : info[2 * BM + 2];
-        // the factor of the row that this thread finishes below (8 threads a row for every rank)
-        const int mine_row = tid >> 3;
+        // the factor of the row that this thread finishes below
+        const int mine_row = tid / TPR;
         float mine_fac = p.scaling ? __ldg(p.scaling + e) : 1.0f;
         if (p.weight && mine_row < rows) mine_fac *= __ldg(p.weight + row0 + mine_row);
 
@@ -892,12 +894,12 @@ __global__ void __launch_bounds__(StreamShape<RP>::kThreads, StreamShape<RP>::kC
                 named_sync(1, kLoraThreads);
             }
         }
-        // Eight threads a row: the sums, times the row's factor, and their 16-bit terms. fp16 terms are
+        // TPR threads a row: the sums, times the row's factor, and their 16-bit terms. fp16 terms are
         // of the row scaled by a power of two, its largest value in [1, 2) (or below, where the whole
         // row is below 2^-24, the type's smallest step), which s_fac takes back.
         {
-            constexpr int PER = RP / 8;
-            const int j0 = PER * (tid & 7);
+            constexpr int PER = RP / TPR;
+            const int j0 = PER * (tid % TPR);
             float v[PER];
             const bool have = mine_row < rows && info[mine_row] >= 0;            // no source row: zeros
             const float* from = s_red + mine_row * S::kRed + j0;
@@ -929,12 +931,12 @@ __global__ void __launch_bounds__(StreamShape<RP>::kThreads, StreamShape<RP>::kC
             }
             if constexpr (F16) {
 #pragma unroll
-                for (int o = 4; o; o >>= 1) big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, o));
+                for (int o = TPR / 2; o; o >>= 1) big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, o));
                 const uint32_t ex = min(max(__float_as_uint(big) >> 23, 103u), 253u);
                 const float shrink = __uint_as_float((254u - ex) << 23);
 #pragma unroll
                 for (int k = 0; k < PER; ++k) v[k] *= shrink;
-                if ((tid & 7) == 0) s_fac[mine_row] = shrink;
+                if (tid % TPR == 0) s_fac[mine_row] = shrink;
             }
 #pragma unroll
             for (int k = 0; k < PER; k += 2) {
@@ -967,9 +969,9 @@ __global__ void __launch_bounds__(StreamShape<RP>::kThreads, StreamShape<RP>::kC
             const uint32_t at = (uint32_t)(slot * S::kStage), factor = ring + at + BM * S::kRow;
             if (!gone && q * CW + n0 < p.O) {
                 // the sums start from base: lane (g, t) has columns 32 s + 8t + 4i + c in o[s][c][2h + i]
-                float o[2][4][4];
+                float o[SUB][4][4];
 #pragma unroll
-                for (int s = 0; s < 2; ++s)
+                for (int s = 0; s < SUB; ++s)
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
                         uint4 bs = make_uint4(0u, 0u, 0u, 0u);
@@ -989,7 +991,7 @@ __global__ void __launch_bounds__(StreamShape<RP>::kThreads, StreamShape<RP>::kC
 #pragma unroll
                 for (int k = 0; k < KS; ++k)
 #pragma unroll
-                    for (int s = 0; s < 2; ++s) {
+                    for (int s = 0; s < SUB; ++s) {
                         uint32_t b[4][2];                            // MMA tile c: columns 4n + c of 32
                         if constexpr (!BWD) {
 #pragma unroll
@@ -1020,7 +1022,7 @@ __global__ void __launch_bounds__(StreamShape<RP>::kThreads, StreamShape<RP>::kC
 #pragma unroll
                 for (int h = 0; h < 2; ++h)
 #pragma unroll
-                    for (int s = 0; s < 2; ++s) {
+                    for (int s = 0; s < SUB; ++s) {
                         uint32_t w[4];
 #pragma unroll
                         for (int i = 0; i < 4; ++i) {
@@ -1040,29 +1042,44 @@ __global__ void __launch_bounds__(StreamShape<RP>::kThreads, StreamShape<RP>::kC
     }
 }
 
-template <int RP, bool BWD, bool F16>
+// at most one partial tile of `rows` rows for every adapter that has a row
+int64_t most_tiles(const LoraRowsArgs& a, int rows) {
+    const int64_t active = a.R < a.L ? a.R : a.L;
+    return active + (a.R - active) / rows;
+}
+
+template <int RP, int ROWS, bool BWD, bool F16>
 cudaError_t launch_stream_t(const LoraRowsArgs& a, cudaStream_t s) {
-    static_assert(StreamShape<RP>::smem(2048) + 256 <= 227 * 1024, "shared memory of a CTA");
+    using S = StreamShape<RP, ROWS>;
+    constexpr size_t most = S::smem(2048) < kMaxSmem ? S::smem(2048) : kMaxSmem;
     static std::atomic<bool> attr_set[64];           // per device: dynamic shared memory opted in
     const int dev = current_device();
     if (!attr_set[dev].load(std::memory_order_acquire)) {
-        const cudaError_t e = cudaFuncSetAttribute(lora_stream_kernel<RP, BWD, F16>,
-                                                   cudaFuncAttributeMaxDynamicSharedMemorySize, (int)StreamShape<RP>::smem(2048));
+        const cudaError_t e = cudaFuncSetAttribute(lora_stream_kernel<RP, ROWS, BWD, F16>,
+                                                   cudaFuncAttributeMaxDynamicSharedMemorySize, (int)most);
         if (e != cudaSuccess) return e;
         attr_set[dev].store(true, std::memory_order_release);
     }
-    const int64_t active = a.R < a.L ? a.R : a.L;
-    const int64_t tiles = active + (a.R - active) / StreamShape<RP>::BM, sms = device_sm_count();
-    const int64_t ctas = sms * StreamShape<RP>::kCtas;
-    lora_stream_kernel<RP, BWD, F16><<<(unsigned)(tiles < ctas ? tiles : ctas), StreamShape<RP>::kThreads,
-                                       StreamShape<RP>::smem(a.L), s>>>(a);
+    const int64_t tiles = most_tiles(a, ROWS), sms = device_sm_count();
+    lora_stream_kernel<RP, ROWS, BWD, F16><<<(unsigned)(tiles < sms ? tiles : sms), S::kThreads, S::smem(a.L), s>>>(a);
     return cudaGetLastError();
 }
 
+template <int RP, int ROWS>
+cudaError_t launch_stream_m(const LoraRowsArgs& a, bool bwd, bool f16, cudaStream_t s) {
+    if (bwd) return launch_stream_t<RP, ROWS, true, false>(a, s);
+    return f16 ? launch_stream_t<RP, ROWS, false, true>(a, s) : launch_stream_t<RP, ROWS, false, false>(a, s);
+}
+
+// Tiles of 64 rows halve what the factors cost and keep more rows in flight, once there are
+// enough of them for two rounds of the SMs (and the adapters' table fits beside a rank of 32)
 template <int RP>
 cudaError_t launch_stream(const LoraRowsArgs& a, bool bwd, bool f16, cudaStream_t s) {
-    if (bwd) return launch_stream_t<RP, true, false>(a, s);
-    return f16 ? launch_stream_t<RP, false, true>(a, s) : launch_stream_t<RP, false, false>(a, s);
+    static_assert(StreamShape<RP, 32>::smem(2048) <= kMaxSmem, "shared memory of a CTA");
+    if constexpr (RP <= 32)
+        if (most_tiles(a, 64) >= 2 * (int64_t)device_sm_count() && StreamShape<RP, 64>::smem(a.L) <= kMaxSmem)
+            return launch_stream_m<RP, 64>(a, bwd, f16, s);
+    return launch_stream_m<RP, 32>(a, bwd, f16, s);
 }
 
 template <int RP, int MT, bool BWD, bool F16>
@@ -1078,9 +1095,7 @@ cudaError_t launch_rows_t(const LoraRowsArgs& a, cudaStream_t s) {
         if (e != cudaSuccess) return e;
         attr_set[dev].store(true, std::memory_order_release);
     }
-    // at most one partial tile for every adapter that has a row
-    const int64_t active = a.R < a.L ? a.R : a.L;
-    const int64_t tiles = active + (a.R - active) / BM;
+    const int64_t tiles = most_tiles(a, BM);
     int cs = 1;
     while (cs < 8 && tiles * cs * 2 <= 2 * (int64_t)device_sm_count()) cs *= 2;
     cudaLaunchConfig_t cfg = {};
@@ -1107,7 +1122,7 @@ cudaError_t launch_rows_m(const LoraRowsArgs& a, bool bwd, bool f16, cudaStream_
 template <int RP>
 cudaError_t launch_rows_r(const LoraRowsArgs& a, bool bwd, bool f16, cudaStream_t s) {
     const int64_t active = a.R < a.L ? a.R : a.L;
-    if constexpr (RP == 32 || RP == 64)
+    if constexpr (RP <= 64)
         if (a.R >= 24 * active && a.R >= 16 * (int64_t)device_sm_count()) return launch_stream<RP>(a, bwd, f16, s);
     return a.R >= 24 * active ? launch_rows_m<RP, 2>(a, bwd, f16, s) : launch_rows_m<RP, 1>(a, bwd, f16, s);
 }

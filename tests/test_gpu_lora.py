@@ -200,6 +200,17 @@ def test_many_rows(counts, r, K, N, dtype):
         p.check_backward(torch.float32, act8=K % 32 == 0)
 
 
+@pytest.mark.parametrize("r", [16, 24])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+def test_rows_for_several_rounds(r, dtype):
+    # tiles of 64 rows, several to an SM, the last of most adapters partial
+    p = Problem([100 + (37 * i) % 101 for i in range(140)] + [0, 1], r, 264, 288, dtype=dtype, seed=r, spare=5)
+    assert p.R > 64 * 2 * 148
+    p.check_forward()
+    if dtype == torch.bfloat16:
+        p.check_backward()
+
+
 def test_many_rows_without_arrays_and_with_bad_ones():
     p = Problem([2600, 0, 77], 16, 264, 200, gather=False, scatter=False, weights=False, scaling=False)
     p.check_forward()
