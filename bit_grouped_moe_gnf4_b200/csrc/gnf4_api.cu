@@ -498,7 +498,7 @@ extern "C" {
 
 const char* gnf4_last_error(void) { return g_err; }
 
-int gnf4_version(void) { return 100; }
+int gnf4_version(void) { return 200; }
 
 gnf4_status gnf4_quantize_nf4(const float* w, int64_t rows, int64_t K, uint8_t* packed,
                               float* absmax, void* stream) {

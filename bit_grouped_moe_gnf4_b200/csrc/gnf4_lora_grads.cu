@@ -1,0 +1,404 @@
+// The gradients of the adapters (gnf4_lora.cuh): sums over an adapter's rows.
+//
+// One gradient of one adapter: sum over its rows of left[r, j] right[row r, n], rows the MMA's
+// contraction index. A CTA owns WC * SC columns (SC a warp) and walks the adapter's rows in
+// stages of 32 WR: the rows of `right` are gathered into shared memory by 16-byte asynchronous
+// copies, three stages deep (the gather's latency, index then row, is what a warp alone cannot
+// hide), while `left` is read ahead by a stage into registers and split into its 16-bit terms
+// once for all warps. Both fragments come out of shared memory transposed.
+//
+// What bounds it is instruction issue: about 330 instructions a warp and stage of 32 rows (the
+// copies' addresses, the split of left, the products; 450 with codes), issue slots 47 % busy
+// and a third of the stalls on loads, with DRAM at a fifth of its rate. 128 experts over 32768
+// rows, rank 16, 2048 checkpointed and 1536 columns: 64 us. Warps that only copy beside warps
+// that only multiply took 65 to 75 us there, with bulk copies of a row (52 to 67 cycles each
+// from one CTA) or 16-byte ones.
+#include <atomic>
+#include <cstdint>
+#include <cuda_runtime.h>
+
+#include "gnf4_act8.cuh"
+#include "gnf4_lora.cuh"
+
+namespace gnf4 {
+
+namespace {
+
+constexpr int kGradStages = 3;
+
+template <int RP, int WR, int TERMS>
+struct GradShape {
+    static constexpr int CT = RP <= 32 ? 8 : 4;          // MMA column tiles of a warp's slab
+    static constexpr int SC = 8 * CT;                    // its columns
+    static constexpr int MT = RP / 16;
+    static constexpr int WC = kLoraWarps / WR;
+    static constexpr int CW = WC * SC;                   // columns of the CTA
+    static constexpr int SR = 32 * WR;                   // rows of a stage
+    static constexpr int kPitch16 = 2 * CW + 16;         // bytes a row in shared memory: bf16,
+    static constexpr int kPitch8 = CW + 16;              // codes; conflict-free fragment loads
+    static constexpr int kPlane = RP + 8;                // elements a row of a term plane
+    static constexpr int kStride = SC + 4;               // floats of a row of the sum
+    static constexpr int kLeft = (SR * RP / 4 + kLoraThreads - 1) / kLoraThreads;   // float4 of left a thread and stage
+    static constexpr size_t stage_bytes = (size_t)SR * kPitch16;
+    static constexpr size_t plane_bytes = (size_t)TERMS * SR * kPlane * 2;          // one of two buffers
+    static constexpr size_t scale_bytes = (size_t)SR * (CW / 32) * 2;               // one of two buffers
+    // codes take half a stage; their steps lie in the other half of the last one
+    static constexpr size_t step_at = kGradStages * stage_bytes - 2 * scale_bytes;
+    static_assert((kGradStages - 1) * stage_bytes + SR * kPitch8 <= step_at, "the steps behind the last stage's codes");
+    static constexpr size_t work = kGradStages * stage_bytes + 2 * plane_bytes + 2 * SR * 4;
+    static constexpr size_t sums = sizeof(float) * (size_t)kLoraWarps * RP * kStride;
+    static constexpr size_t smem = work > sums ? work : sums;
+};
+
+template <int RP, int WR, int TERMS, bool Q8>
+__device__ __forceinline__ void grad_body(const LoraGradArgs& p, const LoraGradSide& d, int e, int col0, uint8_t* smem) {
+    using S = GradShape<RP, WR, TERMS>;
+    constexpr int CT = S::CT, MT = S::MT, WC = S::WC, CW = S::CW, SR = S::SR;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int g = lane >> 2, t = lane & 3;
+    const int wc = warp % WC, wr = warp / WC;
+    const int CS = (int)cluster_size(), crank = (int)cluster_rank();
+    uint8_t* s_stage = smem;
+    uint16_t* s_plane = reinterpret_cast<uint16_t*>(smem + kGradStages * S::stage_bytes);
+    uint16_t* s_step = reinterpret_cast<uint16_t*>(smem + S::step_at);
+    int* s_row = reinterpret_cast<int*>(smem + kGradStages * S::stage_bytes + 2 * S::plane_bytes);
+    const uint32_t stage0 = smem_addr(s_stage), plane0 = smem_addr(s_plane);
+
+    const int64_t lo = clamp_row(p.offsets[e], p.R), hi = clamp_row(p.offsets[e + 1], p.R);
+    const int rows = hi > lo ? (int)(hi - lo) : 0;
+    const float scal = d.factor && p.scaling ? __ldg(p.scaling + e) : 1.0f;
+    // stage i of this CTA: rows first(i) .. first(i) + SR - 1 of the adapter
+    const int stages = (rows + SR * CS - 1) / (SR * CS);
+    auto first = [&](int i) { return (i * CS + crank) * SR; };
+
+    // the row of `right` behind row `local` of the adapter, or -1
+    auto source_row = [&](int local) -> int {
+        if (local >= rows) return -1;
+        const int64_t r = lo + local;
+        const int64_t at = d.row ? (int64_t)__ldg(d.row + r) : r;
+        return at >= 0 && at < d.n ? (int)at : -1;
+    };
+    auto issue = [&](int i) {
+        constexpr int CPR = (Q8 ? CW : 2 * CW) / 16;       // 16-byte pieces of a row
+        const int* row = s_row + (i & 1) * SR;
+        const uint32_t dst = stage0 + (uint32_t)((i % kGradStages) * S::stage_bytes);
+        const int per = Q8 ? 16 : 8;
+        constexpr int PER = SR * CPR / kLoraThreads;
+        int source[PER];                                   // read before any copy is issued, which would hold them up
+#pragma unroll
+        for (int q = 0; q < PER; ++q) source[q] = row[(q * kLoraThreads + tid) / CPR];
+#pragma unroll
+        for (int q = 0; q < PER; ++q) {
+            const int id = q * kLoraThreads + tid, r = id / CPR, c = id % CPR;
+            const int at = source[q];
+            const bool ok = at >= 0 && col0 + c * per < d.C;
+            const void* src = Q8 ? (const void*)(d.codes + (ok ? (int64_t)at * d.C + col0 + c * per : 0))
+                                 : (const void*)(d.right + (ok ? (int64_t)at * d.C + col0 + c * per : 0));
+            copy_async16(dst + (uint32_t)(r * (Q8 ? S::kPitch8 : S::kPitch16) + c * 16), src, ok ? 16u : 0u);
+        }
+    };
+
+    // `left` of the next stage, in registers until the stage before it is being worked on
+    float4 left[S::kLeft];
+    float fac[S::kLeft];
+    uint32_t scale[(SR * (CW / 32) + kLoraThreads - 1) / kLoraThreads];
+    auto fetch = [&](int i) {
+#pragma unroll
+        for (int q = 0; q < S::kLeft; ++q) {
+            const int id = q * kLoraThreads + tid, local = first(i) + id / (RP / 4), j = 4 * (id % (RP / 4));
+            left[q] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            fac[q] = scal;
+            if (id < SR * RP / 4 && local < rows && j < p.r) {
+                const int64_t r = lo + local;
+                left[q] = *reinterpret_cast<const float4*>(d.left + r * p.r + j);
+                if (d.factor && p.weight) fac[q] *= __ldg(p.weight + r);
+            }
+        }
+        if constexpr (Q8) {
+            constexpr int BPR = CW / 32;
+#pragma unroll
+            for (int q = 0; q < (SR * BPR + kLoraThreads - 1) / kLoraThreads; ++q) {
+                const int id = q * kLoraThreads + tid;
+                scale[q] = 0u;
+                if (id < SR * BPR && col0 + 32 * (id % BPR) < d.C) {
+                    const int at = source_row(first(i) + id / BPR);
+                    if (at >= 0) scale[q] = __ldg(d.scales + (int64_t)at * (d.C / 32) + col0 / 32 + id % BPR);
+                }
+            }
+        }
+    };
+    auto place = [&](int i) {
+        uint16_t* plane = s_plane + (i & 1) * (S::plane_bytes / 2);
+#pragma unroll
+        for (int q = 0; q < S::kLeft; ++q) {
+            const int id = q * kLoraThreads + tid;
+            if (id < SR * RP / 4) {
+                uint32_t a[TERMS], b[TERMS];
+                split_pair<TERMS, false>(left[q].x * fac[q], left[q].y * fac[q], a);
+                split_pair<TERMS, false>(left[q].z * fac[q], left[q].w * fac[q], b);
+#pragma unroll
+                for (int k = 0; k < TERMS; ++k)
+                    *reinterpret_cast<uint2*>(plane + (size_t)(k * SR + id / (RP / 4)) * S::kPlane + 4 * (id % (RP / 4))) =
+                        make_uint2(a[k], b[k]);
+            }
+        }
+        if constexpr (Q8) {
+#pragma unroll
+            for (int q = 0; q < (SR * (CW / 32) + kLoraThreads - 1) / kLoraThreads; ++q) {
+                const int id = q * kLoraThreads + tid;
+                if (id < SR * (CW / 32)) s_step[(i & 1) * (S::scale_bytes / 2) + id] = (uint16_t)act8_step_bf16(scale[q]);
+            }
+        }
+    };
+
+    float acc[MT][CT][4];
+#pragma unroll
+    for (int m = 0; m < MT; ++m)
+#pragma unroll
+        for (int c = 0; c < CT; ++c)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) acc[m][c][j] = 0.0f;
+
+    // prologue: two stages of copies under way, the first stage's left in place
+    static_assert(kGradStages == 3, "the prologue and the row buffers are written for three stages");
+    if (tid < SR) {
+        s_row[tid] = source_row(first(0) + tid);
+        s_row[SR + tid] = source_row(first(1) + tid);
+    }
+    __syncthreads();
+    if (stages > 0) issue(0);
+    copy_commit();
+    if (stages > 1) issue(1);
+    copy_commit();
+    int next_row = tid < SR ? source_row(first(2) + tid) : -1;
+    if (!d.factor) wait_for_previous_grid();            // dA's left comes from the rows kernel; the copies do not
+    fetch(0);
+    place(0);
+    fetch(1);
+    __syncthreads();                                    // s_row has been read
+    if (tid < SR) s_row[tid] = next_row;                // stage 2's
+    next_row = tid < SR ? source_row(first(3) + tid) : -1;
+
+    for (int i = 0; i < stages; ++i) {
+        copy_wait<1>();
+        __syncthreads();                                // stage i is there; stage i - 1 is done with
+        if (i + 2 < stages) issue(i + 2);
+        copy_commit();
+        place(i + 1);
+        if (tid < SR) s_row[((i + 3) & 1) * SR + tid] = next_row;
+        fetch(i + 2);
+        next_row = tid < SR ? source_row(first(i + 4) + tid) : -1;
+
+        const uint32_t x = stage0 + (uint32_t)((i % kGradStages) * S::stage_bytes);
+        const uint32_t plane = plane0 + (uint32_t)((i & 1) * S::plane_bytes);
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+            const int r0 = 32 * wr + 16 * half;
+            uint32_t a[MT][TERMS][4];
+#pragma unroll
+            for (int m = 0; m < MT; ++m)
+#pragma unroll
+                for (int k = 0; k < TERMS; ++k)
+                    ldmatrix4_trans(a[m][k], plane + (uint32_t)(((k * SR + r0 + (lane & 7) + 8 * (lane >> 4)) * S::kPlane +
+                                                                 16 * m + 8 * ((lane >> 3) & 1)) * 2));
+            if constexpr (!Q8) {
+#pragma unroll
+                for (int c = 0; c < CT; c += 2) {
+                    uint32_t b[4];                       // two column tiles: rows 0-7 and 8-15 of each
+                    ldmatrix4_trans(b, x + (uint32_t)((r0 + (lane & 15)) * S::kPitch16 +
+                                                      (wc * S::SC + 8 * c + 8 * (lane >> 4)) * 2));
+#pragma unroll
+                    for (int m = 0; m < MT; ++m)
+#pragma unroll
+                        for (int k = 0; k < TERMS; ++k) {
+                            mma_bf16_16816(acc[m][c], a[m][k][0], a[m][k][1], a[m][k][2], a[m][k][3], b[0], b[1]);
+                            mma_bf16_16816(acc[m][c + 1], a[m][k][0], a[m][k][1], a[m][k][2], a[m][k][3], b[2], b[3]);
+                        }
+                }
+            } else {
+                uint32_t code_frag[CT][2];
+                // this lane's rows 2t, 2t+1 and 2t+8, 2t+9, its CT columns from CT g on; MMA tile c takes
+                // column c of them, a byte of either row of a pair, as two bf16 numbers
+#pragma unroll
+                for (int pair = 0; pair < 2; ++pair) {
+                    const int row = r0 + 2 * t + 8 * pair;
+                    const uint32_t at = x + (uint32_t)(row * S::kPitch8 + wc * S::SC + CT * g);
+                    uint32_t w[2][CT / 4];
+                    if constexpr (CT == 8) {
+                        const uint2 u = lds8(at), v = lds8(at + S::kPitch8);
+                        w[0][0] = u.x, w[0][1] = u.y, w[1][0] = v.x, w[1][1] = v.y;
+                    } else {
+                        w[0][0] = lds4(at), w[1][0] = lds4(at + S::kPitch8);
+                    }
+                    const uint16_t* st = s_step + (i & 1) * (S::scale_bytes / 2) + row * (CW / 32) + (wc * S::SC + CT * g) / 32;
+                    const uint32_t step = (uint32_t)st[0] | (uint32_t)st[CW / 32] << 16;
+#pragma unroll
+                    for (int c = 0; c < CT; ++c)
+                        code_frag[c][pair] = act8_pair(prmt(w[0][c / 4], w[1][c / 4], 0x0400u + 0x0101u * (c & 3)), step);
+                }
+#pragma unroll
+                for (int c = 0; c < CT; ++c)
+#pragma unroll
+                    for (int m = 0; m < MT; ++m)
+#pragma unroll
+                        for (int k = 0; k < TERMS; ++k)
+                            mma_bf16_16816(acc[m][c], a[m][k][0], a[m][k][1], a[m][k][2], a[m][k][3], code_frag[c][0], code_frag[c][1]);
+            }
+        }
+    }
+    copy_wait<0>();
+    __syncthreads();                                     // the stages become the sums' space
+
+    // column of the accumulators: tile c, MMA column n is 8 c + n, from codes CT n + c
+    float* s_red = reinterpret_cast<float*>(smem);
+    float* mine = s_red + (size_t)warp * RP * S::kStride;
+#pragma unroll
+    for (int m = 0; m < MT; ++m)
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int c = 0; c < CT; ++c) {
+                float* row = mine + (16 * m + 8 * h + g) * S::kStride;
+                if constexpr (Q8) {
+                    row[CT * (2 * t) + c] = acc[m][c][2 * h];
+                    row[CT * (2 * t + 1) + c] = acc[m][c][2 * h + 1];
+                } else {
+                    *reinterpret_cast<float2*>(row + 8 * c + 2 * t) = make_float2(acc[m][c][2 * h], acc[m][c][2 * h + 1]);
+                }
+            }
+    __syncthreads();
+    if (WR > 1) {
+        for (int i = tid; i < CW * RP; i += kLoraThreads) {
+            const int w = i / (RP * S::SC), at = (i / S::SC % RP) * S::kStride + i % S::SC;
+            float v = s_red[(size_t)w * RP * S::kStride + at];
+#pragma unroll
+            for (int q = 1; q < WR; ++q) v += s_red[(size_t)(q * WC + w) * RP * S::kStride + at];
+            s_red[(size_t)w * RP * S::kStride + at] = v;
+        }
+        __syncthreads();
+    }
+    // the cluster's CTAs share the columns out and add up theirs, in place: no other CTA reads those
+    const int own = CW / CS, own0 = crank * own;
+    if (CS > 1) {
+        cluster_arrive();
+        cluster_wait();
+        for (int i = tid; i < RP * own / 4; i += kLoraThreads) {
+            const int j = i / (own / 4), n = own0 + 4 * (i % (own / 4));
+            float* at = s_red + (size_t)(n / S::SC) * RP * S::kStride + j * S::kStride + n % S::SC;
+            *reinterpret_cast<float4*>(at) = cluster_sum(at, CS);
+        }
+        cluster_arrive();                                // a CTA's sums are read until here
+        __syncthreads();
+    }
+    // eight at a time along the gradient's contiguous axis: its columns (dA) or the rank (dB); C
+    // and r are multiples of 8
+    for (int i = tid; i < own * RP / 8; i += kLoraThreads) {
+        // dA: (rank, columns n..); dB: (column, ranks j..), the pieces of a column's ranks in turn
+        const int j = d.transposed ? 8 * (i % (RP / 8)) : i / (own / 8);
+        const int n = own0 + (d.transposed ? i / (RP / 8) : 8 * (i % (own / 8)));
+        if (j >= p.r || col0 + n >= d.C) continue;
+        const float* at = s_red + (size_t)(n / S::SC) * RP * S::kStride + j * S::kStride + n % S::SC;
+        const int next = d.transposed ? S::kStride : 1;
+        float v[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) v[k] = at[k * next];
+        const int64_t o = (int64_t)e * p.r * d.C + (d.transposed ? (int64_t)(col0 + n) * p.r + j : (int64_t)j * d.C + col0 + n);
+        if constexpr (TERMS == 3) {
+            float4* to = reinterpret_cast<float4*>(reinterpret_cast<float*>(d.out) + o);
+            to[0] = make_float4(v[0], v[1], v[2], v[3]);
+            to[1] = make_float4(v[4], v[5], v[6], v[7]);
+        } else {
+            *reinterpret_cast<uint4*>(reinterpret_cast<uint16_t*>(d.out) + o) =
+                make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
+        }
+    }
+    if (CS > 1) cluster_wait();
+    if (tid == 0) wait_for_previous_grid();              // whoever waits for this grid waits for that one too
+}
+
+// CTAs (or clusters) of one adapter for one gradient; none for a gradient that is not asked for
+__host__ __device__ __forceinline__ int grad_items(const LoraGradSide& d, int cols) {
+    return d.out ? (d.C + cols - 1) / cols : 0;
+}
+
+template <int RP, int WR, int TERMS, bool Q8>
+__global__ void __launch_bounds__(kLoraThreads, RP <= 32 && WR == 1 ? 2 : 1) lora_grads_kernel(const LoraGradArgs p) {
+    extern __shared__ __align__(16) uint8_t smem[];
+    constexpr int CW = GradShape<RP, WR, TERMS>::CW;
+    const int item = (int)(blockIdx.x / cluster_size());
+    const int na = grad_items(p.a, CW), nb = grad_items(p.b, CW);
+    // dB's items come first: they need nothing of the rows kernel and fill the SMs that it leaves
+    if (item < nb * p.L) grad_body<RP, WR, TERMS, false>(p, p.b, item / nb, item % nb * CW, smem);
+    else grad_body<RP, WR, TERMS, Q8>(p, p.a, (item - nb * p.L) / na, (item - nb * p.L) % na * CW, smem);
+}
+
+template <int RP, int WR, int TERMS, bool Q8>
+cudaError_t launch_grads_t(const LoraGradArgs& a, int cs, cudaStream_t s) {
+    using S = GradShape<RP, WR, TERMS>;
+    static_assert(S::smem <= 227 * 1024, "shared memory of a CTA");
+    static std::atomic<bool> attr_set[64];
+    const int dev = current_device();
+    if (!attr_set[dev].load(std::memory_order_acquire)) {
+        const cudaError_t e = cudaFuncSetAttribute(lora_grads_kernel<RP, WR, TERMS, Q8>,
+                                                   cudaFuncAttributeMaxDynamicSharedMemorySize, (int)S::smem);
+        if (e != cudaSuccess) return e;
+        attr_set[dev].store(true, std::memory_order_release);
+    }
+    const int64_t items = (int64_t)a.L * (grad_items(a.a, S::CW) + grad_items(a.b, S::CW));
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(items * cs));
+    cfg.blockDim = dim3(kLoraThreads);
+    cfg.dynamicSmemBytes = S::smem;
+    cfg.stream = s;
+    cudaLaunchAttribute at[2];
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim.x = (unsigned)cs;
+    at[0].val.clusterDim.y = 1;
+    at[0].val.clusterDim.z = 1;
+    at[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[1].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = a.after_rows ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, lora_grads_kernel<RP, WR, TERMS, Q8>, a);
+}
+
+template <int RP, int WR>
+cudaError_t launch_grads_w(const LoraGradArgs& a, bool f32, int cs, cudaStream_t s) {
+    if (a.a.codes) return f32 ? launch_grads_t<RP, WR, 3, true>(a, cs, s) : launch_grads_t<RP, WR, 2, true>(a, cs, s);
+    return f32 ? launch_grads_t<RP, WR, 3, false>(a, cs, s) : launch_grads_t<RP, WR, 2, false>(a, cs, s);
+}
+
+// How the work is cut. First by columns, all the CTA's warps side by side (WR = 1), with a
+// cluster of CTAs along an adapter's rows as long as they fit on the SMs at once and keep 128
+// rows each. Where that leaves more than half of the SMs idle, narrow CTAs whose warps share
+// the rows of a stage. us with events at 2048 and 1536 columns, wide and narrow, best cluster
+// of each: rank 16, one adapter of 4096 rows 25.8 and 19.1, of 512 rows 10.9 and 10.9, four
+// of 1024 rows 17.0 and 19.0, four of 4096 rows 36.9 and 46.0, sixteen of 512 rows 23.8 and
+// 35.3; rank 32 and fp32 results, one of 4096 rows 37.2 and 26.9, four of 4096 rows 64.2 and
+// 76.6; rank 64, one of 4096 rows 29.7 and 39.4.
+template <int RP>
+cudaError_t launch_grads_r(const LoraGradArgs& a, bool f32, cudaStream_t s) {
+    constexpr int WR = RP <= 64 ? 4 : 2;             // at rank 128 four warps' rows do not fit
+    const int64_t active = a.R < a.L ? (a.R > 0 ? a.R : 1) : a.L;
+    const int64_t avg = (a.R + active - 1) / active, sms = device_sm_count();
+    const int64_t wide = active * (grad_items(a.a, GradShape<RP, 1, 2>::CW) + grad_items(a.b, GradShape<RP, 1, 2>::CW));
+    const int64_t narrow = active * (grad_items(a.a, GradShape<RP, WR, 2>::CW) + grad_items(a.b, GradShape<RP, WR, 2>::CW));
+    const int64_t room = RP <= 32 ? 2 * sms : sms;   // CTAs that run at once
+    int cs = 1;
+    while (cs < 8 && wide * cs * 2 <= room && avg >= 128 * 2 * cs) cs *= 2;
+    if (2 * wide * cs >= room || narrow > sms) return launch_grads_w<RP, 1>(a, f32, cs, s);
+    cs = 1;
+    while (cs < 8 && narrow * cs * 2 <= sms && avg >= 128 * 2 * cs) cs *= 2;
+    return launch_grads_w<RP, WR>(a, f32, cs, s);
+}
+
+}  // namespace
+
+cudaError_t launch_lora_grads(const LoraGradArgs& a, bool f32, cudaStream_t s) {
+    if (a.r <= 16) return launch_grads_r<16>(a, f32, s);
+    if (a.r <= 32) return launch_grads_r<32>(a, f32, s);
+    if (a.r <= 64) return launch_grads_r<64>(a, f32, s);
+    return launch_grads_r<128>(a, f32, s);
+}
+
+}  // namespace gnf4
