@@ -731,6 +731,7 @@ gnf4_status gnf4_lora_apply(const void* base, const void* x, int dtype, const vo
     if (st != GNF4_OK || R == 0) return st;
     if ((st = check_lora_buffers(c)) != GNF4_OK) return st;
     if (!x || !out) return fail(GNF4_ERR_INVALID_ARG, "null pointer argument");
+    if (out == x) return fail(GNF4_ERR_INVALID_ARG, "out may be base, but not x");
     if (!aligned16(x) || !aligned16(base) || !aligned16(out) || !aligned16(h))
         return fail(GNF4_ERR_MISALIGNED, "x, base, out and h must be 16-byte aligned");
     if ((st = check_lora_device(c)) != GNF4_OK || (st = check_device({x, base, out, h})) != GNF4_OK) return st;
@@ -775,6 +776,7 @@ gnf4_status gnf4_lora_backward(const void* grad_out, const void* x, const int8_t
     if (R > 0) {
         if ((st = check_lora_buffers(c)) != GNF4_OK) return st;
         if (!grad_out || !h || !grad_h || (dx_base && !dx)) return fail(GNF4_ERR_INVALID_ARG, "null pointer argument");
+        if (grad_h == h || dx == grad_out) return fail(GNF4_ERR_INVALID_ARG, "grad_h may not be h, nor dx grad_out");
         if ((st = check_lora_x(x, x_codes, x_scales, !dA)) != GNF4_OK) return st;
     } else if (!adapter_offsets || !aligned8(adapter_offsets)) {
         return fail(GNF4_ERR_INVALID_ARG, "adapter_offsets must be given, 8-byte aligned");

@@ -434,11 +434,12 @@ gnf4_status gnf4_swiglu_backward(const void* grad_out, const void* gate_up, cons
  *            a row whose token or destination is out of range counts as zeros or is not written
  * scaling    device fp32 [L], or NULL
  * h          device fp32 [R, r], or NULL: the rows h, which gnf4_lora_backward wants
+ * Outputs may not overlap inputs, except that out may be base.
  * L in [1, 2048], r in [8, 128] with r % 8 == 0, K and N multiples of 8 up to 2^24, R at most
- * 2^30. 16-bit buffers and h are
- * 16-byte aligned, row arrays and scaling 4-byte, offsets 8-byte. Sums in fp32; h enters the
- * second product with about 17 significant bits (two 16-bit terms). Deterministic: the same
- * call gives the same bits. R == 0 launches nothing and accepts NULL buffers.
+ * 2^30. 16-bit buffers and h are 16-byte aligned, row arrays and scaling 4-byte, offsets 8-byte.
+ * Sums in fp32; h enters the second product with about 17 significant bits (two 16-bit terms).
+ * Deterministic: the same call gives the same bits. R == 0 launches nothing and accepts NULL
+ * buffers.
  * flags: 0 or GNF4_CHECK (validates offsets, row arrays and weights on the device first: one
  * extra kernel and a stream sync).
  * Errors: INVALID_ARG, UNSUPPORTED_SHAPE, MISALIGNED, DEVICE_STATUS (GNF4_CHECK), CUDA.
@@ -468,6 +469,7 @@ gnf4_status gnf4_lora_apply(const void* base, const void* x, int dtype, const vo
  * dA, dB     device [L, r, K] and [L, N, r] of grad_dtype: GNF4_DTYPE_BF16 or GNF4_DTYPE_F32
  *            (fp32 sums, rounded once). dA may be NULL, and then x is not given either: a
  *            layer that has x back only later takes it from gnf4_lora_grad_a
+ * Outputs may not overlap inputs or one another, except that dx may be dx_base.
  * Other arguments, limits and errors as in gnf4_lora_apply. Rows at or behind
  * adapter_offsets[L] of dx and grad_h are not written. With R == 0 the gradients are written
  * as zeros (adapter_offsets, dA and dB must then still be given).

@@ -10,13 +10,14 @@ from bit_grouped_moe_gnf4_b200 import _lib
 from bit_grouped_moe_gnf4_b200._lib import lib
 
 FAKE = 0x7f0000001000          # 16-byte aligned, never dereferenced: validation fails first
+FAKE2 = FAKE + 4096
 INVALID, SHAPE, MISALIGNED, OK = (_lib.GNF4_ERR_INVALID_ARG, _lib.GNF4_ERR_UNSUPPORTED_SHAPE,
                                   _lib.GNF4_ERR_MISALIGNED, _lib.GNF4_OK)
 
 
 def apply(**kw):
     a = dict(base=FAKE, x=FAKE, dtype=0, A=FAKE, B=FAKE, off=FAKE, tok=None, wt=None, dst=None, scal=None, L=4, r=16,
-             N=128, K=256, R=8, T_in=8, T_out=8, out=FAKE, h=None, flags=0)
+             N=128, K=256, R=8, T_in=8, T_out=8, out=FAKE2, h=None, flags=0)
     assert set(kw) <= set(a)
     a.update(kw)
     return lib.gnf4_lora_apply(*a.values(), None)
@@ -24,7 +25,7 @@ def apply(**kw):
 
 def backward(**kw):
     a = dict(g=FAKE, x=FAKE, xc=None, xs=None, h=FAKE, A=FAKE, B=FAKE, off=FAKE, tok=None, wt=None, src=None, scal=None,
-             L=4, r=16, N=128, K=256, R=8, T_in=8, T_g=8, dxb=FAKE, dx=FAKE, gh=FAKE, dA=FAKE, dB=FAKE, gdt=0, flags=0)
+             L=4, r=16, N=128, K=256, R=8, T_in=8, T_g=8, dxb=FAKE, dx=FAKE2, gh=FAKE2, dA=FAKE, dB=FAKE, gdt=0, flags=0)
     assert set(kw) <= set(a)
     a.update(kw)
     return lib.gnf4_lora_backward(*a.values(), None)
@@ -44,7 +45,8 @@ COMMON = [
 
 @pytest.mark.parametrize("kw,status", COMMON + [
     (dict(dtype=2), INVALID), (dict(out=None), INVALID), (dict(T_out=7), INVALID), (dict(base=FAKE + 8), MISALIGNED),
-    (dict(out=FAKE + 4), MISALIGNED), (dict(dst=FAKE + 2), MISALIGNED),
+    (dict(out=FAKE + 4), MISALIGNED), (dict(out=FAKE), INVALID),         # x itself
+    (dict(dst=FAKE + 2), MISALIGNED),
     (dict(), INVALID),                                   # not device memory
     (dict(R=0, x=None, base=None, out=None, A=None, B=None, off=None), OK),
 ])
@@ -57,6 +59,7 @@ def test_apply_refusals(kw, status):
     (dict(gdt=1), INVALID), (dict(g=None), INVALID), (dict(h=None), INVALID), (dict(gh=None), INVALID),
     (dict(dA=None), INVALID), (dict(dB=None), INVALID),      # dA NULL: x must be as well
     (dict(dx=None), INVALID),                                # dx_base without dx
+    (dict(gh=FAKE), INVALID), (dict(dx=FAKE, dxb=None), INVALID),        # h and grad_out themselves
     (dict(T_g=7), INVALID), (dict(xc=FAKE, xs=FAKE), INVALID), (dict(x=None, xc=FAKE), INVALID),
     (dict(x=None, xs=FAKE), INVALID), (dict(x=None, xc=FAKE, xs=FAKE, K=264), SHAPE),
     (dict(x=None, xc=FAKE + 8, xs=FAKE), MISALIGNED), (dict(g=FAKE + 2), MISALIGNED), (dict(dx=FAKE + 8), MISALIGNED),

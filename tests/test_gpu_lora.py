@@ -211,6 +211,15 @@ def test_rows_for_several_rounds(r, dtype):
         p.check_backward()
 
 
+@pytest.mark.parametrize("r,K,N", [(8, 8, 8), (16, 40, 24), (32, 8, 16), (64, 16, 8)])
+def test_many_rows_of_narrow_axes_and_many_adapters(r, K, N):
+    p = Problem([2] * 2048, r, K, N, seed=r)
+    p.check_forward()
+    p.check_backward()
+    Problem([13] * 2000, r, K, N, dtype=torch.float16, seed=r).check_forward()      # a table that leaves no room for 64 rows
+    Problem([3000], r, K, N, seed=r).check_backward(torch.float32)
+
+
 def test_many_rows_without_arrays_and_with_bad_ones():
     p = Problem([2600, 0, 77], 16, 264, 200, gather=False, scatter=False, weights=False, scaling=False)
     p.check_forward()
