@@ -312,9 +312,8 @@ def combine_topk(y: torch.Tensor, T: int, k: int, row_of_slot: Optional[torch.Te
 def _shaped(t: Optional[torch.Tensor], shape, dtype: torch.dtype, name: str, like: torch.Tensor) -> torch.Tensor:
     """``t`` checked against a type and shape, or a new tensor beside ``like`` if it is None."""
     if t is None:
-        if like.dtype is dtype:
-            return torch.empty_like(like) if like.shape == shape else like.new_empty(shape)
-        return like.new_empty(shape, dtype=dtype)
+        # beside one of its own shape a tensor is made faster
+        return torch.empty_like(like, dtype=dtype) if like.shape == shape else like.new_empty(shape, dtype=dtype)
     _need(t, dtype, name)
     if t.shape != shape:
         raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
@@ -338,8 +337,6 @@ def quantize_act8(x: torch.Tensor, codes: Optional[torch.Tensor] = None, scales:
     ``[..., K//32]``), one e8m0 scale per 32 elements (include/gnf4.h)."""
     _need(x, torch.bfloat16, "x")
     K = x.shape[-1]
-    if codes is None:
-        codes = torch.empty_like(x, dtype=torch.int8)
     codes = _shaped(codes, x.shape, torch.int8, "codes", x)
     scales = _shaped(scales, (*x.shape[:-1], K // 32), torch.uint8, "scales", x)
     check(lib.gnf4_quantize_act8(_ptr(x), x.numel() // K if K else 0, K, _ptr(codes), _ptr(scales), _stream(stream)),
@@ -355,8 +352,6 @@ def dequantize_act8(codes: torch.Tensor, scales: torch.Tensor, out: Optional[tor
     _need(scales, torch.uint8, "scales")
     if scales.shape != (*codes.shape[:-1], K // 32):
         raise ValueError(f"scales must be [..., {K // 32}] beside codes {list(codes.shape)}, got {list(scales.shape)}")
-    if out is None:
-        out = torch.empty_like(codes, dtype=torch.bfloat16)
     out = _shaped(out, codes.shape, torch.bfloat16, "out", codes)
     check(lib.gnf4_dequantize_act8(_ptr(codes), _ptr(scales), codes.numel() // K if K else 0, K, _ptr(out),
                                    _stream(stream)), "gnf4_dequantize_act8")
@@ -372,8 +367,6 @@ def swiglu_act8(gate_up: torch.Tensor, out: Optional[torch.Tensor] = None, codes
         raise ValueError(f"gate_up must be [R, 2I], got {tuple(gate_up.shape)}")
     R, I = gate_up.shape[0], gate_up.shape[1] // 2
     out = _shaped(out, (R, I), torch.bfloat16, "out", gate_up)
-    if codes is None:
-        codes = torch.empty_like(gate_up, dtype=torch.int8)
     codes = _shaped(codes, (R, 2 * I), torch.int8, "codes", gate_up)
     scales = _shaped(scales, (R, 2 * I // 32), torch.uint8, "scales", gate_up)
     check(lib.gnf4_swiglu_act8(_ptr(gate_up), R, I, _ptr(out), _ptr(codes), _ptr(scales), _stream(stream)),
