@@ -829,6 +829,7 @@ gnf4_status gnf4_lora_backward(const void* grad_out, const void* x, const int8_t
     q.R = R;
     q.L = (int)L;
     q.r = (int)r;
+    q.heavy = 0;
     q.after_rows = R > 0;
     cudaError_t e = launch_lora_grads(q, grad_dtype == GNF4_DTYPE_F32, s);
     return e == cudaSuccess ? GNF4_OK : cuda_fail(e, "lora_backward gradient launch");

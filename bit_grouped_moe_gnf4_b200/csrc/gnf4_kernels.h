@@ -106,6 +106,7 @@ struct LoraGradArgs {
     const float* scaling;       // [L] or null
     int64_t R;
     int L, r;
+    int heavy;                  // set by the launch: more rows than this are shared by a cluster; 0: see the kernel
     int after_rows;             // a.left comes from the rows kernel launched just before on the stream
 };
 cudaError_t launch_lora_grads(const LoraGradArgs& a, bool f32, cudaStream_t s);

@@ -50,14 +50,16 @@ struct GradShape {
     static constexpr size_t smem = work > sums ? work : sums;
 };
 
+// Part `part` of `parts` of the rows of adapter e, columns col0 on; more than one part are those of
+// the CTAs of a cluster.
 template <int RP, int WR, int TERMS, bool Q8>
-__device__ __forceinline__ void grad_body(const LoraGradArgs& p, const LoraGradSide& d, int e, int col0, uint8_t* smem) {
+__device__ __forceinline__ void grad_body(const LoraGradArgs& p, const LoraGradSide& d, int e, int col0, int parts, int part,
+                                          uint8_t* smem) {
     using S = GradShape<RP, WR, TERMS>;
     constexpr int CT = S::CT, MT = S::MT, WC = S::WC, CW = S::CW, SR = S::SR;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int g = lane >> 2, t = lane & 3;
     const int wc = warp % WC, wr = warp / WC;
-    const int CS = (int)cluster_size(), crank = (int)cluster_rank();
     uint8_t* s_stage = smem;
     uint16_t* s_plane = reinterpret_cast<uint16_t*>(smem + kGradStages * S::stage_bytes);
     uint16_t* s_step = reinterpret_cast<uint16_t*>(smem + S::step_at);
@@ -68,8 +70,8 @@ __device__ __forceinline__ void grad_body(const LoraGradArgs& p, const LoraGradS
     const int rows = hi > lo ? (int)(hi - lo) : 0;
     const float scal = d.factor && p.scaling ? __ldg(p.scaling + e) : 1.0f;
     // stage i of this CTA: rows first(i) .. first(i) + SR - 1 of the adapter
-    const int stages = (rows + SR * CS - 1) / (SR * CS);
-    auto first = [&](int i) { return (i * CS + crank) * SR; };
+    const int stages = (rows + SR * parts - 1) / (SR * parts);
+    auto first = [&](int i) { return (i * parts + part) * SR; };
 
     // the row of `right` behind row `local` of the adapter, or -1
     auto source_row = [&](int local) -> int {
@@ -278,14 +280,14 @@ __device__ __forceinline__ void grad_body(const LoraGradArgs& p, const LoraGradS
         __syncthreads();
     }
     // the cluster's CTAs share the columns out and add up theirs, in place: no other CTA reads those
-    const int own = CW / CS, own0 = crank * own;
-    if (CS > 1) {
+    const int own = CW / parts, own0 = part * own;
+    if (parts > 1) {
         cluster_arrive();
         cluster_wait();
         for (int i = tid; i < RP * own / 4; i += kLoraThreads) {
             const int j = i / (own / 4), n = own0 + 4 * (i % (own / 4));
             float* at = s_red + (size_t)(n / S::SC) * RP * S::kStride + j * S::kStride + n % S::SC;
-            *reinterpret_cast<float4*>(at) = cluster_sum(at, CS);
+            *reinterpret_cast<float4*>(at) = cluster_sum(at, parts);
         }
         cluster_arrive();                                // a CTA's sums are read until here
         __syncthreads();
@@ -312,8 +314,7 @@ __device__ __forceinline__ void grad_body(const LoraGradArgs& p, const LoraGradS
                 make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
         }
     }
-    if (CS > 1) cluster_wait();
-    if (tid == 0) wait_for_previous_grid();              // whoever waits for this grid waits for that one too
+    if (parts > 1) cluster_wait();
 }
 
 // CTAs (or clusters) of one adapter for one gradient; none for a gradient that is not asked for
@@ -321,15 +322,68 @@ __host__ __device__ __forceinline__ int grad_items(const LoraGradSide& d, int co
     return d.out ? (d.C + cols - 1) / cols : 0;
 }
 
+// A cluster has one unit of the work. Without p.heavy a unit is an item (an adapter's columns for
+// one of the gradients), its rows shared by the cluster's CTAs. With p.heavy, the items of adapters
+// of more rows than that are such units, and the others' items go one to a CTA: a routing that
+// prefers a few adapters would leave the whole call waiting for the CTAs of the largest. dB's
+// units come first: they need nothing of the rows kernel and fill the SMs that it leaves.
 template <int RP, int WR, int TERMS, bool Q8>
 __global__ void __launch_bounds__(kLoraThreads, RP <= 32 && WR == 1 ? 2 : 1) lora_grads_kernel(const LoraGradArgs p) {
     extern __shared__ __align__(16) uint8_t smem[];
     constexpr int CW = GradShape<RP, WR, TERMS>::CW;
-    const int item = (int)(blockIdx.x / cluster_size());
+    const int CS = (int)cluster_size(), crank = (int)cluster_rank();
     const int na = grad_items(p.a, CW), nb = grad_items(p.b, CW);
-    // dB's items come first: they need nothing of the rows kernel and fill the SMs that it leaves
-    if (item < nb * p.L) grad_body<RP, WR, TERMS, false>(p, p.b, item / nb, item % nb * CW, smem);
-    else grad_body<RP, WR, TERMS, Q8>(p, p.a, (item - nb * p.L) / na, (item - nb * p.L) % na * CW, smem);
+    int unit = (int)(blockIdx.x / CS), e, n, item;
+    bool side_b, shared = true;
+    if (p.heavy == 0) {
+        side_b = unit < p.L * nb;
+        n = side_b ? nb : na;
+        item = side_b ? unit : unit - p.L * nb;
+        e = item / n;
+    } else {
+        // the heavy adapters, counted over runs of neighbouring ones, a run a thread
+        __shared__ int s_warp[kLoraWarps], s_adapter;
+        const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+        const int per = (p.L + kLoraThreads - 1) / kLoraThreads;
+        const int e0 = min(tid * per, p.L), e1 = min(e0 + per, p.L);
+        auto is_heavy = [&](int q) { return clamp_row(p.offsets[q + 1], p.R) - clamp_row(p.offsets[q], p.R) > p.heavy; };
+        int mine = 0;
+        for (int q = e0; q < e1; ++q) mine += is_heavy(q);
+        int upto = mine;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int v = __shfl_up_sync(0xffffffffu, upto, o);
+            if (lane >= o) upto += v;
+        }
+        if (lane == 31) s_warp[warp] = upto;
+        if (tid == 0) s_adapter = p.L;
+        __syncthreads();
+        int heavy = 0, before = upto - mine;
+#pragma unroll
+        for (int w = 0; w < kLoraWarps; ++w) {
+            before += w < warp ? s_warp[w] : 0;
+            heavy += s_warp[w];
+        }
+        const int units_b = heavy * nb + ((p.L - heavy) * nb + CS - 1) / CS;
+        side_b = unit < units_b;
+        n = side_b ? nb : na;
+        item = side_b ? unit : unit - units_b;
+        shared = item < heavy * n;
+        if (!shared) item = (item - heavy * n) * CS + crank;
+        // the item's adapter is the item / n-th of the heavy ones, or of the others
+        int k = n ? item / n - (shared ? before : e0 - before) : -1;
+        if (k >= 0 && k < (shared ? mine : e1 - e0 - mine))
+            for (int q = e0; q < e1; ++q)
+                if (is_heavy(q) == shared && k-- == 0) s_adapter = q;
+        __syncthreads();
+        e = s_adapter;
+    }
+    if (e < p.L) {
+        const int col0 = item % n * CW, parts = shared ? CS : 1, part = shared ? crank : 0;
+        if (side_b) grad_body<RP, WR, TERMS, false>(p, p.b, e, col0, parts, part, smem);
+        else grad_body<RP, WR, TERMS, Q8>(p, p.a, e, col0, parts, part, smem);
+    }
+    if (threadIdx.x == 0) wait_for_previous_grid();      // whoever waits for this grid waits for that one too
 }
 
 template <int RP, int WR, int TERMS, bool Q8>
@@ -344,9 +398,15 @@ cudaError_t launch_grads_t(const LoraGradArgs& a, int cs, cudaStream_t s) {
         if (e != cudaSuccess) return e;
         attr_set[dev].store(true, std::memory_order_release);
     }
-    const int64_t items = (int64_t)a.L * (grad_items(a.a, S::CW) + grad_items(a.b, S::CW));
+    const int na = grad_items(a.a, S::CW), nb = grad_items(a.b, S::CW);
+    int64_t clusters = (int64_t)a.L * (na + nb);
+    if (a.heavy) {                                       // as many as the rows can make
+        const int64_t heavy = a.R / a.heavy < a.L ? a.R / a.heavy : a.L;
+        const int64_t more = heavy * (na + nb) + (a.L * (int64_t)nb + cs - 1) / cs + (a.L * (int64_t)na + cs - 1) / cs;
+        clusters = more < clusters ? more : clusters;
+    }
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(items * cs));
+    cfg.gridDim = dim3((unsigned)(clusters * cs));
     cfg.blockDim = dim3(kLoraThreads);
     cfg.dynamicSmemBytes = S::smem;
     cfg.stream = s;
@@ -386,7 +446,19 @@ cudaError_t launch_grads_r(const LoraGradArgs& a, bool f32, cudaStream_t s) {
     const int64_t room = RP <= 32 ? 2 * sms : sms;   // CTAs that run at once
     int cs = 1;
     while (cs < 8 && wide * cs * 2 <= room && avg >= 128 * 2 * cs) cs *= 2;
-    if (2 * wide * cs >= room || narrow > sms) return launch_grads_w<RP, 1>(a, f32, cs, s);
+    if (2 * wide * cs >= room || narrow > sms) {
+        if (cs > 1 || avg < 32) return launch_grads_w<RP, 1>(a, f32, cs, s);
+        // One CTA an item: adapters of four times the average's rows get a cluster. us at 2048 and
+        // 1536 columns, without and with it, the routing uniform and then with shares like 1 / e:
+        // rank 16, 128 adapters, 32768 rows 126 to 135 and 257 to 141; 64 adapters, 4096 rows 34 to
+        // 37 and 50 to 37; rank 64, 64 adapters, 8192 rows 112 to 118 and 135 to 117; at 10 rows
+        // an adapter (rank 32) 46 to 50 and 51 to 52. Clusters of 2 leave the second 257 at 177, of
+        // 8 at 152; at rank 64, where an SM has one CTA, clusters of 4 leave the 112 and 135 at 129
+        // and 135.
+        LoraGradArgs b = a;
+        b.heavy = (int)(4 * avg > 256 ? 4 * avg : 256);
+        return launch_grads_w<RP, 1>(b, f32, RP <= 32 ? 4 : 2, s);
+    }
     cs = 1;
     while (cs < 8 && narrow * cs * 2 <= sms && avg >= 128 * 2 * cs) cs *= 2;
     return launch_grads_w<RP, WR>(a, f32, cs, s);

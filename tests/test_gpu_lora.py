@@ -247,6 +247,31 @@ def test_long_segments_split_over_a_cluster():
         Problem([m], 16, 136, 72, seed=m).check_backward(torch.float32)
 
 
+@pytest.mark.parametrize("r,K,N", [(16, 608, 576), (8, 72, 40), (32, 520, 1032), (64, 264, 776), (128, 200, 264)])
+@pytest.mark.parametrize("heavy", [(0,), (99,), (3, 4, 50), tuple(range(7))])
+def test_a_few_adapters_have_most_rows(heavy, r, K, N):
+    # a hundred adapters and more; those of many rows are shared by CTAs, alone or in a row, the first or the last
+    counts = [1400 if i in heavy else i % 41 for i in range(100)]
+    p = Problem(counts, r, K, N, seed=r, spare=1700)
+    p.check_backward(torch.float32 if len(heavy) > 1 else torch.bfloat16, act8=K % 32 == 0)
+
+
+@pytest.mark.parametrize("many", [300, 1300])
+def test_a_few_of_many_adapters_have_most_rows(many):
+    # runs of adapters to a thread
+    counts = [2500 if i in (1, 299, 600, 1299) else 30 + i % 5 for i in range(many)]
+    p = Problem(counts, 16, 96, 64, seed=many)
+    p.check_backward()
+    a = p.check_backward()
+    assert all(torch.equal(u, v) for u, v in zip(a, p.check_backward()))
+
+
+def test_half_of_the_adapters_have_most_rows():
+    # as many of more than four times the average as there can be, and an average that spare rows raise
+    Problem([257, 0, 0, 0, 0] * 30, 16, 520, 264, seed=1).check_backward()
+    Problem([300, 1] * 60, 24, 520, 264, seed=2, spare=90).check_backward(torch.float32)
+
+
 def test_in_place_and_deterministic():
     p = Problem([7, 0, 50, 1], 16, 256, 320)
     out, _ = p.forward()
