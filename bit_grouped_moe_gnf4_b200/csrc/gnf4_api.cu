@@ -592,11 +592,13 @@ gnf4_status gnf4_device_status(void* stream) {
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     cudaError_t e = cudaStreamSynchronize(s);
     if (e != cudaSuccess) return cuda_fail(e, "stream synchronize");
-    cudaError_t e1 = cudaSuccess, e2 = cudaSuccess, e3 = cudaSuccess;
-    const unsigned d = take_decode_error(&e1), pr = take_prefill_error(&e2), lo = take_lora_error(&e3);
+    cudaError_t e1 = cudaSuccess, e2 = cudaSuccess, e3 = cudaSuccess, e4 = cudaSuccess;
+    const unsigned d = take_decode_error(&e1), pr = take_prefill_error(&e2);
+    const unsigned lo = take_lora_error(&e3) | take_grads_error(&e4) << 4;
     if (e1 != cudaSuccess) return cuda_fail(e1, "read device status");
     if (e2 != cudaSuccess) return cuda_fail(e2, "read device status");
     if (e3 != cudaSuccess) return cuda_fail(e3, "read device status");
+    if (e4 != cudaSuccess) return cuda_fail(e4, "read device status");
     if (d | pr | lo)
         return fail(GNF4_ERR_DEVICE_STATUS, "a kernel gave up waiting on a barrier (decode 0x%x, prefill 0x%x, adapters 0x%x)",
                     d, pr, lo);

@@ -124,5 +124,6 @@ int current_device();
 unsigned take_decode_error(cudaError_t* err);
 unsigned take_prefill_error(cudaError_t* err);
 unsigned take_lora_error(cudaError_t* err);
+unsigned take_grads_error(cudaError_t* err);
 
 }  // namespace gnf4

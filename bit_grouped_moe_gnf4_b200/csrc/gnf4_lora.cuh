@@ -7,9 +7,10 @@
 // The forward, and the first line of the backward, are one chain of two products: the
 // backward's has A and B swapped and both read along their other axis. Few rows go through
 // gnf4_lora_rows.cu, many through gnf4_lora_stream.cu; the sums over an adapter's rows are in
-// gnf4_lora_grads.cu. The rank is small, so all of it is bound by the rows it streams, by the
-// adapters' bytes, or by latency; the products run on warp-level MMAs, which take 8 cycles of
-// a scheduler each and keep the tensor pipe below a third everywhere.
+// gnf4_lora_grads.cu and, for ranks above 32, gnf4_lora_grads_wide.cu. The rank is small, so all of
+// it is bound by the rows it streams, by the adapters' bytes, or by latency. The products run on
+// warp-level MMAs, which take 8 cycles of a scheduler each and keep the tensor pipe below a
+// third everywhere, but for the sums of the larger ranks, which run on tcgen05.
 //
 // Rounding: sums are fp32. h (and g) enter the second product as two 16-bit terms, the value's
 // rounding and that of its remainder: about 17 significant bits, so that what the caller sees

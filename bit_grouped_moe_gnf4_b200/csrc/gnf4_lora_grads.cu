@@ -13,12 +13,11 @@
 // rows, rank 16, 2048 checkpointed and 1536 columns: 64 us. Warps that only copy beside warps
 // that only multiply took 65 to 75 us there, with bulk copies of a row (52 to 67 cycles each
 // from one CTA) or 16-byte ones.
-#include <atomic>
 #include <cstdint>
 #include <cuda_runtime.h>
 
 #include "gnf4_act8.cuh"
-#include "gnf4_lora.cuh"
+#include "gnf4_lora_grads.cuh"
 
 namespace gnf4 {
 
@@ -28,7 +27,7 @@ constexpr int kGradStages = 3;
 
 template <int RP, int WR, int TERMS>
 struct GradShape {
-    static constexpr int CT = RP <= 32 ? 8 : 4;          // MMA column tiles of a warp's slab
+    static constexpr int CT = 8;                         // MMA column tiles of a warp's slab
     static constexpr int SC = 8 * CT;                    // its columns
     static constexpr int MT = RP / 16;
     static constexpr int WC = kLoraWarps / WR;
@@ -50,11 +49,10 @@ struct GradShape {
     static constexpr size_t smem = work > sums ? work : sums;
 };
 
-// Part `part` of `parts` of the rows of adapter e, columns col0 on; more than one part are those of
-// the CTAs of a cluster.
+// One item; more than one part of its rows are those of the CTAs of a cluster.
 template <int RP, int WR, int TERMS, bool Q8>
-__device__ __forceinline__ void grad_body(const LoraGradArgs& p, const LoraGradSide& d, int e, int col0, int parts, int part,
-                                          uint8_t* smem) {
+__device__ __forceinline__ void grad_body(const LoraGradArgs& p, const LoraGradSide& d, const GradItem& it, uint8_t* smem) {
+    const int e = it.e, col0 = it.col0, parts = it.parts, part = it.part;
     using S = GradShape<RP, WR, TERMS>;
     constexpr int CT = S::CT, MT = S::MT, WC = S::WC, CW = S::CW, SR = S::SR;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -317,71 +315,14 @@ __device__ __forceinline__ void grad_body(const LoraGradArgs& p, const LoraGradS
     if (parts > 1) cluster_wait();
 }
 
-// CTAs (or clusters) of one adapter for one gradient; none for a gradient that is not asked for
-__host__ __device__ __forceinline__ int grad_items(const LoraGradSide& d, int cols) {
-    return d.out ? (d.C + cols - 1) / cols : 0;
-}
-
-// A cluster has one unit of the work. Without p.heavy a unit is an item (an adapter's columns for
-// one of the gradients), its rows shared by the cluster's CTAs. With p.heavy, the items of adapters
-// of more rows than that are such units, and the others' items go one to a CTA: a routing that
-// prefers a few adapters would leave the whole call waiting for the CTAs of the largest. dB's
-// units come first: they need nothing of the rows kernel and fill the SMs that it leaves.
 template <int RP, int WR, int TERMS, bool Q8>
-__global__ void __launch_bounds__(kLoraThreads, RP <= 32 && WR == 1 ? 2 : 1) lora_grads_kernel(const LoraGradArgs p) {
+__global__ void __launch_bounds__(kLoraThreads, WR == 1 ? 2 : 1) lora_grads_kernel(const LoraGradArgs p) {
     extern __shared__ __align__(16) uint8_t smem[];
-    constexpr int CW = GradShape<RP, WR, TERMS>::CW;
-    const int CS = (int)cluster_size(), crank = (int)cluster_rank();
-    const int na = grad_items(p.a, CW), nb = grad_items(p.b, CW);
-    int unit = (int)(blockIdx.x / CS), e, n, item;
-    bool side_b, shared = true;
-    if (p.heavy == 0) {
-        side_b = unit < p.L * nb;
-        n = side_b ? nb : na;
-        item = side_b ? unit : unit - p.L * nb;
-        e = item / n;
-    } else {
-        // the heavy adapters, counted over runs of neighbouring ones, a run a thread
-        __shared__ int s_warp[kLoraWarps], s_adapter;
-        const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-        const int per = (p.L + kLoraThreads - 1) / kLoraThreads;
-        const int e0 = min(tid * per, p.L), e1 = min(e0 + per, p.L);
-        auto is_heavy = [&](int q) { return clamp_row(p.offsets[q + 1], p.R) - clamp_row(p.offsets[q], p.R) > p.heavy; };
-        int mine = 0;
-        for (int q = e0; q < e1; ++q) mine += is_heavy(q);
-        int upto = mine;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int v = __shfl_up_sync(0xffffffffu, upto, o);
-            if (lane >= o) upto += v;
-        }
-        if (lane == 31) s_warp[warp] = upto;
-        if (tid == 0) s_adapter = p.L;
-        __syncthreads();
-        int heavy = 0, before = upto - mine;
-#pragma unroll
-        for (int w = 0; w < kLoraWarps; ++w) {
-            before += w < warp ? s_warp[w] : 0;
-            heavy += s_warp[w];
-        }
-        const int units_b = heavy * nb + ((p.L - heavy) * nb + CS - 1) / CS;
-        side_b = unit < units_b;
-        n = side_b ? nb : na;
-        item = side_b ? unit : unit - units_b;
-        shared = item < heavy * n;
-        if (!shared) item = (item - heavy * n) * CS + crank;
-        // the item's adapter is the item / n-th of the heavy ones, or of the others
-        int k = n ? item / n - (shared ? before : e0 - before) : -1;
-        if (k >= 0 && k < (shared ? mine : e1 - e0 - mine))
-            for (int q = e0; q < e1; ++q)
-                if (is_heavy(q) == shared && k-- == 0) s_adapter = q;
-        __syncthreads();
-        e = s_adapter;
-    }
-    if (e < p.L) {
-        const int col0 = item % n * CW, parts = shared ? CS : 1, part = shared ? crank : 0;
-        if (side_b) grad_body<RP, WR, TERMS, false>(p, p.b, e, col0, parts, part, smem);
-        else grad_body<RP, WR, TERMS, Q8>(p, p.a, e, col0, parts, part, smem);
+    __shared__ GradSearch find;
+    const GradItem it = grad_item(p, GradShape<RP, WR, TERMS>::CW, &find);
+    if (it.e < p.L) {
+        if (it.side_b) grad_body<RP, WR, TERMS, false>(p, p.b, it, smem);
+        else grad_body<RP, WR, TERMS, Q8>(p, p.a, it, smem);
     }
     if (threadIdx.x == 0) wait_for_previous_grid();      // whoever waits for this grid waits for that one too
 }
@@ -389,37 +330,8 @@ __global__ void __launch_bounds__(kLoraThreads, RP <= 32 && WR == 1 ? 2 : 1) lor
 template <int RP, int WR, int TERMS, bool Q8>
 cudaError_t launch_grads_t(const LoraGradArgs& a, int cs, cudaStream_t s) {
     using S = GradShape<RP, WR, TERMS>;
-    static_assert(S::smem <= 227 * 1024, "shared memory of a CTA");
-    static std::atomic<bool> attr_set[64];
-    const int dev = current_device();
-    if (!attr_set[dev].load(std::memory_order_acquire)) {
-        const cudaError_t e = cudaFuncSetAttribute(lora_grads_kernel<RP, WR, TERMS, Q8>,
-                                                   cudaFuncAttributeMaxDynamicSharedMemorySize, (int)S::smem);
-        if (e != cudaSuccess) return e;
-        attr_set[dev].store(true, std::memory_order_release);
-    }
-    const int na = grad_items(a.a, S::CW), nb = grad_items(a.b, S::CW);
-    int64_t clusters = (int64_t)a.L * (na + nb);
-    if (a.heavy) {                                       // as many as the rows can make
-        const int64_t heavy = a.R / a.heavy < a.L ? a.R / a.heavy : a.L;
-        const int64_t more = heavy * (na + nb) + (a.L * (int64_t)nb + cs - 1) / cs + (a.L * (int64_t)na + cs - 1) / cs;
-        clusters = more < clusters ? more : clusters;
-    }
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(clusters * cs));
-    cfg.blockDim = dim3(kLoraThreads);
-    cfg.dynamicSmemBytes = S::smem;
-    cfg.stream = s;
-    cudaLaunchAttribute at[2];
-    at[0].id = cudaLaunchAttributeClusterDimension;
-    at[0].val.clusterDim.x = (unsigned)cs;
-    at[0].val.clusterDim.y = 1;
-    at[0].val.clusterDim.z = 1;
-    at[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    at[1].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = at;
-    cfg.numAttrs = a.after_rows ? 2 : 1;
-    return cudaLaunchKernelEx(&cfg, lora_grads_kernel<RP, WR, TERMS, Q8>, a);
+    static_assert(S::smem <= kMaxSmem, "shared memory of a CTA");
+    return launch_grads_kernel<lora_grads_kernel<RP, WR, TERMS, Q8>>(a, S::CW, cs, (int)S::smem, s);
 }
 
 template <int RP, int WR>
@@ -435,29 +347,27 @@ cudaError_t launch_grads_w(const LoraGradArgs& a, bool f32, int cs, cudaStream_t
 // of each: rank 16, one adapter of 4096 rows 25.8 and 19.1, of 512 rows 10.9 and 10.9, four
 // of 1024 rows 17.0 and 19.0, four of 4096 rows 36.9 and 46.0, sixteen of 512 rows 23.8 and
 // 35.3; rank 32 and fp32 results, one of 4096 rows 37.2 and 26.9, four of 4096 rows 64.2 and
-// 76.6; rank 64, one of 4096 rows 29.7 and 39.4.
+// 76.6.
 template <int RP>
 cudaError_t launch_grads_r(const LoraGradArgs& a, bool f32, cudaStream_t s) {
-    constexpr int WR = RP <= 64 ? 4 : 2;             // at rank 128 four warps' rows do not fit
+    constexpr int WR = 4;
     const int64_t active = a.R < a.L ? (a.R > 0 ? a.R : 1) : a.L;
     const int64_t avg = (a.R + active - 1) / active, sms = device_sm_count();
     const int64_t wide = active * (grad_items(a.a, GradShape<RP, 1, 2>::CW) + grad_items(a.b, GradShape<RP, 1, 2>::CW));
     const int64_t narrow = active * (grad_items(a.a, GradShape<RP, WR, 2>::CW) + grad_items(a.b, GradShape<RP, WR, 2>::CW));
-    const int64_t room = RP <= 32 ? 2 * sms : sms;   // CTAs that run at once
+    const int64_t room = 2 * sms;                    // wide CTAs that run at once
     int cs = 1;
     while (cs < 8 && wide * cs * 2 <= room && avg >= 128 * 2 * cs) cs *= 2;
     if (2 * wide * cs >= room || narrow > sms) {
         if (cs > 1 || avg < 32) return launch_grads_w<RP, 1>(a, f32, cs, s);
-        // One CTA an item: adapters of four times the average's rows get a cluster. us at 2048 and
-        // 1536 columns, without and with it, the routing uniform and then with shares like 1 / e:
-        // rank 16, 128 adapters, 32768 rows 126 to 135 and 257 to 141; 64 adapters, 4096 rows 34 to
-        // 37 and 50 to 37; rank 64, 64 adapters, 8192 rows 112 to 118 and 135 to 117; at 10 rows
-        // an adapter (rank 32) 46 to 50 and 51 to 52. Clusters of 2 leave the second 257 at 177, of
-        // 8 at 152; at rank 64, where an SM has one CTA, clusters of 4 leave the 112 and 135 at 129
-        // and 135.
+        // One CTA an item: adapters of four times the average's rows get a cluster. us of a backward
+        // pass at 2048 and 1536 columns, without and with it, the routing uniform and then with shares
+        // like 1 / e: 128 adapters, 32768 rows, rank 16 126 to 135 and 257 to 141; 64 adapters, 4096
+        // rows 34 to 37 and 50 to 37; at 10 rows an adapter (rank 32) 46 to 50 and 51 to 52.
+        // Clusters of 2 leave that 257 at 177, of 8 at 152.
         LoraGradArgs b = a;
         b.heavy = (int)(4 * avg > 256 ? 4 * avg : 256);
-        return launch_grads_w<RP, 1>(b, f32, RP <= 32 ? 4 : 2, s);
+        return launch_grads_w<RP, 1>(b, f32, 4, s);
     }
     cs = 1;
     while (cs < 8 && narrow * cs * 2 <= sms && avg >= 128 * 2 * cs) cs *= 2;
@@ -469,8 +379,7 @@ cudaError_t launch_grads_r(const LoraGradArgs& a, bool f32, cudaStream_t s) {
 cudaError_t launch_lora_grads(const LoraGradArgs& a, bool f32, cudaStream_t s) {
     if (a.r <= 16) return launch_grads_r<16>(a, f32, s);
     if (a.r <= 32) return launch_grads_r<32>(a, f32, s);
-    if (a.r <= 64) return launch_grads_r<64>(a, f32, s);
-    return launch_grads_r<128>(a, f32, s);
+    return launch_lora_grads_wide(a, f32, s);
 }
 
 }  // namespace gnf4

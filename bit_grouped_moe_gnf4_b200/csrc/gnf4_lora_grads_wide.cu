@@ -1,0 +1,415 @@
+// The gradients of the adapters for ranks above 32 (gnf4_lora_grads.cu has the formula),
+// on the tensor cores' own memory.
+//
+// A CTA owns CW columns of one gradient of one adapter and walks the adapter's rows in stages of
+// 32. D [terms x rank, CW] += left^T right, rows the contraction index: both operands lie in
+// shared memory as they come, row by row, contiguous across the contraction, and one thread has
+// tcgen05.mma read them there. The terms of `left` are rows of one MMA side by side (128 in all,
+// three terms of rank 64 take two and of rank 128 three) and are added up at the end, when the
+// accumulator leaves tensor memory. The rows of `right` are copied straight to their swizzled
+// place by 16-byte asynchronous copies, two stages ahead; codes and `left` go through the threads
+// that copied them, which make bf16 of the one and the terms of the other.
+//
+// Against warp-level MMAs, which read every fragment through registers: at rank 64, 2048 and 1536
+// columns, 64 adapters, 8192 rows, a backward pass of 87 us instead of 118; one adapter of 4096
+// rows 50 and 71; rank 128, 100 adapters, 4096 rows 229 and 258. At rank 16 their fragments are
+// few, and the parts that stay (a CTA's start, the split of left, the last sum) cost more than
+// they do: 155 and 135 us with 128 adapters, 32768 rows, so that ranks up to 32 keep them. What
+// bounds it there is issue: 54 M instructions, the tensor pipe at 14 %. Persistent CTAs whose
+// copies run on into the next item: 84 us instead of 87 above, but 103 and not 90 with shares
+// like 1 / e, and 145 and not 137 at rank 128 (64 adapters, 8192 rows, 1024 columns).
+#include <cstdint>
+#include <cuda_runtime.h>
+
+#include "gnf4_act8.cuh"
+#include "gnf4_lora_grads.cuh"
+
+namespace gnf4 {
+
+namespace {
+
+constexpr int kGradRows = 32;                            // rows of a stage
+
+template <int RP, int TERMS, bool Q8>
+struct GradShape {
+    static constexpr int CW = RP == 64 ? 256 : 128;       // columns of a CTA, two of which share an SM
+    static constexpr int S = 3;                          // stages
+    static constexpr int MM = 128;                       // rows of an MMA
+    static constexpr int SLOTS = MM / RP;                // terms that fit into one
+    static constexpr int MMAS = (TERMS + SLOTS - 1) / SLOTS;
+    static constexpr int kLeft = (kGradRows * RP / 4 + kLoraThreads - 1) / kLoraThreads;   // float4 of left a thread and stage
+    static constexpr int tile = kGradRows * CW * 2;      // bytes of the rows' columns as bf16
+    static constexpr int raw = Q8 ? tile / 2 : tile;     // as they are copied
+    static constexpr int left = kGradRows * RP * 4, weight = kGradRows * RP;
+    static constexpr int stage = (raw + left + weight + 1023) / 1024 * 1024;
+    static constexpr int plane = MMAS * MM * kGradRows * 2;
+    static constexpr int made = plane + (Q8 ? tile : 0);
+    static constexpr int kStride = CW + 4;               // floats of a row of the sums
+    static constexpr int work = S * stage + made, sums = 4 * RP * kStride;
+    // so much at least that no more CTAs share an SM than its 512 columns of tensor memory serve:
+    // one that waited for columns would hold up its cluster, and clusters could so wait for
+    // one another
+    static constexpr int least = CW * 456 - 1024;
+    static constexpr int need = 128 + 1023 + (work > sums ? work : sums);       // behind GradControl, at a multiple of 1024
+    static constexpr int smem = need > least ? need : least;
+};
+
+struct GradControl {
+    uint64_t done;                                       // the MMAs of a stage are through
+    uint32_t tmem;
+    int abort;
+    GradSearch find;
+};
+static_assert(sizeof(GradControl) <= 128, "the space before the stages");
+
+__device__ unsigned g_grads_err;                         // set when a wait gives up
+
+// A matrix in shared memory for the tensor cores, contiguous along M or N: atoms of 8 rows (of K)
+// by 64 elements, swizzled by 128 bytes; `next` bytes to the next 64 elements, 1024 to the next 8 rows.
+__device__ __forceinline__ uint64_t desc_across(uint32_t saddr, uint32_t next) {
+    return (uint64_t)((saddr >> 4) & 0x3FFFu) | (uint64_t)(next >> 4) << 16 | (uint64_t)(1024 >> 4) << 32 | (uint64_t)1 << 46 |
+           (uint64_t)2 << 61;
+}
+// byte of element m, row k of such a matrix of `rows` rows
+__device__ __forceinline__ uint32_t across(int m, int k, int rows) {
+    return (uint32_t)((m >> 6) * (rows * 128) + k * 128 + ((((m & 63) >> 3) ^ (k & 7)) << 4) + (m & 7) * 2);
+}
+__device__ __forceinline__ void tc_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tc_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void copy_async4(uint32_t dst, const void* src) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
+}
+
+// One item; more than one part of its rows are those of the CTAs of a cluster.
+template <int RP, int TERMS, bool Q8>
+__device__ __forceinline__ void grad_body(const LoraGradArgs& p, const LoraGradSide& d, const GradItem& it, uint8_t* smem,
+                                          GradControl* ctl) {
+    const int e = it.e, col0 = it.col0, parts = it.parts, part = it.part;
+    using S = GradShape<RP, TERMS, Q8>;
+    constexpr int CW = S::CW, SR = kGradRows, D = S::S - 1;     // stages that the copies are ahead
+    constexpr int LPR = S::raw / SR / 16, RPI = 32 / LPR;    // lanes that copy a row, rows a warp copies at a time
+    constexpr int BPR = CW / 32;                             // a row's blocks of a checkpoint
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const uint32_t stage0 = smem_addr(smem), made0 = stage0 + S::S * S::stage;
+
+    const int64_t lo = clamp_row(p.offsets[e], p.R), hi = clamp_row(p.offsets[e + 1], p.R);
+    const int rows = hi > lo ? (int)(hi - lo) : 0;
+    const float scal = d.factor && p.scaling ? __ldg(p.scaling + e) : 1.0f;
+    const float* weight = d.factor ? p.weight : nullptr;
+    // stage i of this CTA: rows first(i) .. first(i) + SR - 1 of the adapter
+    const int stages = (rows + SR * parts - 1) / (SR * parts);
+    auto first = [&](int i) { return (i * parts + part) * SR; };
+
+    // A warp copies rows 8 s + warp of a stage, s = 0..3. Lane 4 j + s knows where row s of the
+    // j-th of eight stages lies in `right` (-1: nowhere).
+    auto source_rows = [&](int i0) -> int {
+        const int local = first(i0 + (lane >> 2)) + 8 * (lane & 3) + warp;
+        if (local >= rows) return -1;
+        const int64_t r = lo + local, at = d.row ? (int64_t)__ldg(d.row + r) : r;
+        return at >= 0 && at < d.n ? (int)at : -1;
+    };
+    // and that row's scales, a byte each
+    uint32_t scale_now[(BPR + 3) / 4], scale_next[(BPR + 3) / 4];
+    auto scales_of = [&](int at, uint32_t (&out)[(BPR + 3) / 4]) {
+#pragma unroll
+        for (int w = 0; w < (BPR + 3) / 4; ++w) out[w] = 0u;
+#pragma unroll
+        for (int b = 0; b < BPR; ++b)
+            if (at >= 0 && col0 + 32 * b < d.C)
+                out[b / 4] |= (uint32_t)__ldg(d.scales + (int64_t)at * (d.C / 32) + col0 / 32 + b) << 8 * (b & 3);
+    };
+
+    // a copied piece: codes wait where their own thread finds them again, bf16 in the MMA's order
+    const int chunk = lane % LPR, sub = lane / LPR;
+    const int col = col0 + chunk * (Q8 ? 16 : 8);
+    const bool col_ok = col < d.C;
+    auto copy_right = [&](int i, int row) {
+        const uint32_t dst = stage0 + (uint32_t)(i % S::S * S::stage);
+#pragma unroll
+        for (int q = 0; q < 4 / RPI; ++q) {
+            const int s = q * RPI + sub;
+            const int at = __shfl_sync(0xffffffffu, row, 4 * (i & 7) + s);
+            const bool ok = at >= 0 && col_ok;
+            const int64_t o = ok ? (int64_t)at * d.C + col : 0;
+            if constexpr (Q8) copy_async16(dst + (uint32_t)((q * kLoraThreads + tid) * 16), d.codes + o, ok ? 16u : 0u);
+            else copy_async16(dst + across(8 * chunk, 8 * s + warp, SR), d.right + o, ok ? 16u : 0u);
+        }
+    };
+    // left, four elements a piece, and the row's weight: read again by the thread that copied them
+    auto copy_left = [&](int i) {
+        const uint32_t dst = stage0 + (uint32_t)(i % S::S * S::stage + S::raw);
+#pragma unroll
+        for (int q = 0; q < S::kLeft; ++q) {
+            const int id = q * kLoraThreads + tid, local = first(i) + id / (RP / 4), j = 4 * (id % (RP / 4));
+            if (id < SR * RP / 4) {
+                const bool ok = local < rows && j < p.r;
+                copy_async16(dst + (uint32_t)(id * 16), d.left + (ok ? (lo + local) * p.r + j : 0), ok ? 16u : 0u);
+                if (weight && ok) copy_async4(dst + (uint32_t)(S::left + id * 4), weight + lo + local);
+            }
+        }
+    };
+    // the stage's left, split into terms: matrix row SLOT * RP + j of MMA q holds term q * SLOTS + SLOT
+    auto make_left = [&](int i) {
+        const uint32_t from = stage0 + (uint32_t)(i % S::S * S::stage + S::raw);
+        const uint32_t to = made0;
+#pragma unroll
+        for (int q = 0; q < S::kLeft; ++q) {
+            const int id = q * kLoraThreads + tid, k = id / (RP / 4), j = 4 * (id % (RP / 4));
+            if (id >= SR * RP / 4) break;
+            const uint4 v = lds16(from + (uint32_t)(id * 16));
+            float f = first(i) + k < rows ? scal : 0.0f;
+            if (weight && first(i) + k < rows) f *= __uint_as_float(lds4(from + (uint32_t)(S::left + id * 4)));
+            uint32_t a[TERMS], b[TERMS];
+            split_pair<TERMS, false>(__uint_as_float(v.x) * f, __uint_as_float(v.y) * f, a);
+            split_pair<TERMS, false>(__uint_as_float(v.z) * f, __uint_as_float(v.w) * f, b);
+#pragma unroll
+            for (int t = 0; t < TERMS; ++t) {
+                const uint32_t at = to + (uint32_t)(t / S::SLOTS * S::MM * SR * 2) + across(t % S::SLOTS * RP + j, k, SR);
+                asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(at), "r"(a[t]), "r"(b[t]) : "memory");
+            }
+        }
+    };
+    // the stage's codes as bf16
+    auto make_right = [&](int i) {
+        const uint32_t from = stage0 + (uint32_t)(i % S::S * S::stage);
+        const uint32_t to = made0 + S::plane;
+#pragma unroll
+        for (int q = 0; q < 4 / RPI; ++q) {
+            const int s = q * RPI + sub;
+            uint32_t sc = 0u;
+#pragma unroll
+            for (int w = 0; w < (BPR + 3) / 4; ++w) {
+                const uint32_t v = __shfl_sync(0xffffffffu, scale_now[w], 4 * (i & 7) + s);
+                if (w == chunk / 8) sc = v;
+            }
+            const uint32_t step = act8_step_bf16(sc >> 8 * (chunk / 2 & 3) & 255u) * 0x10001u;
+            const uint4 v = lds16(from + (uint32_t)((q * kLoraThreads + tid) * 16));
+            const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+            uint32_t o[8];
+#pragma unroll
+            for (int c = 0; c < 8; ++c) o[c] = act8_pair(prmt(u[c / 2], 0u, c & 1 ? 0x0302u : 0x0100u), step);
+#pragma unroll
+            for (int c = 0; c < 2; ++c)
+                asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(to + across(16 * chunk + 8 * c, 8 * s + warp, SR)),
+                             "r"(o[4 * c]), "r"(o[4 * c + 1]), "r"(o[4 * c + 2]), "r"(o[4 * c + 3]) : "memory");
+        }
+    };
+
+    // prologue: D stages of copies under way
+    int row_now = -1, row_next = -1;
+    if (stages > 0) row_now = source_rows(0);
+    if (stages > 8) row_next = source_rows(8);
+#pragma unroll
+    for (int i = 0; i < D; ++i)
+        if (i < stages) copy_right(i, row_now);
+    if constexpr (Q8) scales_of(row_now, scale_now);
+    if (!d.factor) wait_for_previous_grid();             // dA's left comes from the rows kernel; the copies above do not
+#pragma unroll
+    for (int i = 0; i < D; ++i) {
+        if (i < stages) copy_left(i);
+        copy_commit();
+    }
+    if constexpr (TERMS % S::SLOTS != 0 && S::MMAS > 1) {    // the rows of the last MMA that no term fills
+        for (int i = tid; i < (S::MMAS * S::SLOTS - TERMS) * RP * SR * 2 / 16; i += kLoraThreads)
+            *reinterpret_cast<uint4*>(smem + S::S * S::stage + TERMS * RP * SR * 2 + i * 16) = make_uint4(0, 0, 0, 0);
+    }
+
+    const uint32_t tmem = ctl->tmem;
+    bool gone = false;
+    auto wait_made = [&](int i) {                        // the MMAs of stage i are through
+        if (!gone) gone = !mbar_wait_bounded(smem_addr(&ctl->done), (uint32_t)(i & 1), &ctl->abort, &g_grads_err, 1u);
+    };
+    for (int i = 0; i < stages; ++i) {
+        copy_wait<D - 1>();
+        if (i > 0) wait_made(i - 1);
+        if ((i + D & 7) == 0) {
+            row_now = row_next;
+            row_next = i + D + 8 < stages ? source_rows(i + D + 8) : -1;
+        }
+        if (i + D < stages) {
+            copy_right(i + D, row_now);
+            copy_left(i + D);
+        }
+        copy_commit();
+        make_left(i);
+        if constexpr (Q8) {
+            if (i && (i & 7) == 0) {
+#pragma unroll
+                for (int w = 0; w < (BPR + 3) / 4; ++w) scale_now[w] = scale_next[w];
+            }
+            if ((i & 7) == 4) scales_of(row_next, scale_next);
+            make_right(i);
+        }
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        __syncthreads();
+        if (tid == 0 && !gone) {
+            tc_after();
+            const uint32_t a = made0;
+            const uint32_t b = Q8 ? a + S::plane : stage0 + (uint32_t)(i % S::S * S::stage);
+            // fp32 sums of bf16 products; both operands contiguous across K
+            constexpr uint32_t idesc = 1u << 4 | 1u << 7 | 1u << 10 | 1u << 15 | 1u << 16 | (uint32_t)(CW / 8) << 17 | (uint32_t)(S::MM / 16) << 24;
+#pragma unroll
+            for (int k = 0; k < SR / 16; ++k)
+#pragma unroll
+                for (int m = 0; m < S::MMAS; ++m)
+                    asm volatile(
+                        "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+                        " tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n"
+                        ::"r"(tmem), "l"(desc_across(a + (uint32_t)(m * S::MM * SR * 2 + k * 2048), SR * 128)),
+                          "l"(desc_across(b + (uint32_t)(k * 2048), SR * 128)), "r"(idesc), "r"((uint32_t)(i | k | m)) : "memory");
+            asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];"
+                         ::"r"(smem_addr(&ctl->done)) : "memory");
+        }
+    }
+    copy_wait<0>();
+    if (stages > 0) wait_made(stages - 1);
+    tc_after();
+    __syncthreads();                                     // the stages become the sums' space
+
+    // the accumulator, a matrix row a lane; its terms are added up one after the other
+    float* s_red = reinterpret_cast<float*>(smem);
+    const int quarter = warp & 3, half = warp >> 2;      // lanes and columns that this warp reads
+    const int m = 32 * quarter + lane, slot = 32 * quarter / RP;
+#pragma unroll
+    for (int t = 0; t < (TERMS < S::SLOTS ? TERMS : S::SLOTS); ++t) {
+        if (slot == t) {
+#pragma unroll
+            for (int c0 = 0; c0 < CW / 2; c0 += 16) {
+                const int c = half * (CW / 2) + c0;
+                uint32_t v[16];
+                asm volatile(
+                    "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+                    : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]),
+                      "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15])
+                    : "r"(tmem + ((uint32_t)(32 * quarter) << 16) + (uint32_t)c));
+                asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+                float4* to = reinterpret_cast<float4*>(s_red + (m - slot * RP) * S::kStride + c);
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    float4 f = t ? to[k] : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                    if (stages > 0) {                // else nothing was ever written there
+                        f.x += __uint_as_float(v[4 * k]);
+                        f.y += __uint_as_float(v[4 * k + 1]);
+                        f.z += __uint_as_float(v[4 * k + 2]);
+                        f.w += __uint_as_float(v[4 * k + 3]);
+                    }
+                    to[k] = f;
+                }
+            }
+        }
+        __syncthreads();
+    }
+    // the cluster's CTAs share the columns out and add up theirs, in place: no other CTA reads those
+    const int own = CW / parts, own0 = part * own;
+    if (parts > 1) {
+        cluster_arrive();
+        cluster_wait();
+        for (int i = tid; i < RP * own / 4; i += kLoraThreads) {
+            float* at = s_red + i / (own / 4) * S::kStride + own0 + 4 * (i % (own / 4));
+            *reinterpret_cast<float4*>(at) = cluster_sum(at, parts);
+        }
+        cluster_arrive();                                // a CTA's sums are read until here
+        __syncthreads();
+    }
+    // eight at a time along the gradient's contiguous axis: its columns (dA) or the rank (dB); C
+    // and r are multiples of 8
+    for (int i = tid; i < own * RP / 8; i += kLoraThreads) {
+        // dA: (rank, columns n..); dB: (column, ranks j..), the pieces of a column's ranks in turn
+        const int j = d.transposed ? 8 * (i % (RP / 8)) : i / (own / 8);
+        const int n = own0 + (d.transposed ? i / (RP / 8) : 8 * (i % (own / 8)));
+        if (j >= p.r || col0 + n >= d.C) continue;
+        const float* at = s_red + j * S::kStride + n;
+        const int next = d.transposed ? S::kStride : 1;
+        float v[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) v[k] = at[k * next];
+        const int64_t o = (int64_t)e * p.r * d.C + (d.transposed ? (int64_t)(col0 + n) * p.r + j : (int64_t)j * d.C + col0 + n);
+        if constexpr (TERMS == 3) {
+            float4* to = reinterpret_cast<float4*>(reinterpret_cast<float*>(d.out) + o);
+            to[0] = make_float4(v[0], v[1], v[2], v[3]);
+            to[1] = make_float4(v[4], v[5], v[6], v[7]);
+        } else {
+            *reinterpret_cast<uint4*>(reinterpret_cast<uint16_t*>(d.out) + o) =
+                make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
+        }
+    }
+    if (parts > 1) cluster_wait();
+}
+
+template <int RP, int TERMS, bool Q8>
+__global__ void __launch_bounds__(kLoraThreads, 2) lora_grads_wide_kernel(const LoraGradArgs p) {
+    extern __shared__ __align__(1024) uint8_t smem[];
+    uint8_t* buffers = smem + ((0u - smem_addr(smem) - (uint32_t)sizeof(GradControl) & 1023u) + sizeof(GradControl));
+    constexpr int CW = GradShape<RP, TERMS, Q8>::CW;
+    GradControl* ctl = reinterpret_cast<GradControl*>(smem);
+    if (threadIdx.x < 32) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(&ctl->tmem)), "n"(CW) : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
+    if (threadIdx.x == 0) {
+        mbar_init(smem_addr(&ctl->done), 1);
+        ctl->abort = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    tc_before();
+    __syncthreads();
+    tc_after();
+    const GradItem it = grad_item(p, CW, &ctl->find);
+    if (it.e < p.L) {
+        if (it.side_b) grad_body<RP, TERMS, false>(p, p.b, it, buffers, ctl);
+        else grad_body<RP, TERMS, Q8>(p, p.a, it, buffers, ctl);
+    }
+    tc_before();
+    __syncthreads();
+    tc_after();
+    if (threadIdx.x < 32) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(ctl->tmem), "n"(CW));
+    if (threadIdx.x == 0) wait_for_previous_grid();      // whoever waits for this grid waits for that one too
+}
+
+template <int RP, int TERMS, bool Q8>
+cudaError_t launch_wide_t(const LoraGradArgs& a, int cs, cudaStream_t s) {
+    constexpr int own = GradShape<RP, TERMS, Q8>::smem, other = GradShape<RP, TERMS, false>::smem;
+    constexpr int smem = own > other ? own : other;
+    static_assert(2 * (smem + 1024) <= 228 * 1024, "shared memory of an SM");
+    return launch_grads_kernel<lora_grads_wide_kernel<RP, TERMS, Q8>>(a, GradShape<RP, TERMS, Q8>::CW, cs, smem, s);
+}
+
+template <int RP>
+cudaError_t launch_wide_w(const LoraGradArgs& a, bool f32, int cs, cudaStream_t s) {
+    if (a.a.codes) return f32 ? launch_wide_t<RP, 3, true>(a, cs, s) : launch_wide_t<RP, 2, true>(a, cs, s);
+    return f32 ? launch_wide_t<RP, 3, false>(a, cs, s) : launch_wide_t<RP, 2, false>(a, cs, s);
+}
+
+// A cluster along an adapter's rows as long as they fit on the SMs at once and keep 128 rows each
+// (one adapter of 512 rows, rank 128: 44 us, and 48 with 64 rows each). Else adapters of four
+// times the average's rows share a cluster of 2, which is an SM: of 4, 93 us and not 87 in the
+// first case above, 98 and not 90 with shares like 1 / e.
+template <int RP>
+cudaError_t launch_wide_r(const LoraGradArgs& a, bool f32, cudaStream_t s) {
+    constexpr int CW = GradShape<RP, 2, false>::CW;
+    const int64_t active = a.R < a.L ? (a.R > 0 ? a.R : 1) : a.L;
+    const int64_t avg = (a.R + active - 1) / active, room = 2 * (int64_t)device_sm_count();
+    const int64_t items = active * (grad_items(a.a, CW) + grad_items(a.b, CW));
+    int cs = 1;
+    while (cs < 8 && items * cs * 2 <= room && avg >= 128 * 2 * cs) cs *= 2;
+    if (cs > 1 || avg < 32) return launch_wide_w<RP>(a, f32, cs, s);
+    LoraGradArgs b = a;
+    b.heavy = (int)(4 * avg > 256 ? 4 * avg : 256);
+    return launch_wide_w<RP>(b, f32, 2, s);
+}
+
+}  // namespace
+
+unsigned take_grads_error(cudaError_t* err) {
+    unsigned v = 0;
+    const unsigned zero = 0;
+    *err = cudaMemcpyFromSymbol(&v, g_grads_err, sizeof(v));
+    if (*err == cudaSuccess && v) *err = cudaMemcpyToSymbol(g_grads_err, &zero, sizeof(zero));
+    return v;
+}
+
+cudaError_t launch_lora_grads_wide(const LoraGradArgs& a, bool f32, cudaStream_t s) {
+    return a.r <= 64 ? launch_wide_r<64>(a, f32, s) : launch_wide_r<128>(a, f32, s);
+}
+
+}  // namespace gnf4
