@@ -501,6 +501,66 @@ def test_captured_calls_replay_and_share_nothing():
             assert all(torch.equal(a, b) for a, b in zip(out, p.step()))
 
 
+@pytest.mark.parametrize("r", [64, 128])
+def test_large_ranks_captured_beside_projections_on_another_stream(r):
+    # the gradient sums and the projections both keep accumulators in tensor memory
+    g = lib()
+    p = Problem([700, 0, 90, 1500], r, 520, 776, seed=r)
+    many = Problem([1400 if i == 3 else i % 41 for i in range(100)], r, 264, 200, seed=r)
+    Wd, Sd, _, _ = build_stack("nf4", 4, 256, 512)
+    x = torch.randn(4096, 512, device="cuda").to(torch.bfloat16)
+    off = torch.tensor([0, 1000, 1000, 3000, 4096], device="cuda")
+    want_y = g.grouped_gemm("nf4", x, Wd, Sd, off, R=4096)
+    steps = []
+    for q in (p, many):
+        dy, h = torch.randn_like(q.base), torch.randn(q.R, r, device="cuda")
+        steps.append(lambda q=q, dy=dy, h=h: g.lora_backward(dy, h, q.A, q.B, q.offsets, x=q.x, row_src=q.dest, **q.rows()))
+    want = [step() for step in steps]
+    torch.cuda.synchronize()
+    graph, outs = torch.cuda.CUDAGraph(), []
+    with torch.cuda.graph(graph):
+        for step in steps:
+            outs.append(step())
+    side = torch.cuda.Stream()
+    for turn in range(3):
+        for out in outs:
+            for t in out:
+                t.zero_()
+        torch.cuda.synchronize()
+        with torch.cuda.stream(side):
+            ys = [g.grouped_gemm("nf4", x, Wd, Sd, off, R=4096) for _ in range(4)]
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(y, want_y) for y in ys)
+        for got, ref in zip(outs, want):
+            assert all(torch.equal(u, v) for u, v in zip(got, ref))
+    g.device_status()
+
+
+@pytest.mark.parametrize("r", [40, 64, 128])
+@pytest.mark.parametrize("act8", [False, True])
+def test_large_ranks_of_few_and_many_columns_and_rows(r, act8):
+    # stages of 32 rows: one row, a last one short, eight and more of them, a cluster's unequal shares
+    for counts, K, N in (([1], 32, 8), ([32, 33, 31], 288, 264), ([257, 0, 300], 96, 520), ([1029], 544, 128), ([4100, 7], 64, 72)):
+        p = Problem(counts, r, K, N, seed=r + len(counts), spare=2)
+        p.check_backward(torch.float32, act8)
+        p.check_backward(torch.bfloat16, act8)
+
+
+def test_large_rank_rows_that_are_not_finite_stay_in_their_adapter():
+    g = lib()
+    for r in (48, 128):
+        p = Problem([50, 40, 3], r, 96, 64, gather=False, scatter=False)
+        dy, h = torch.randn_like(p.base), torch.randn(p.R, r, device="cuda")
+        clean = g.lora_backward(dy, h, p.A, p.B, p.offsets, x=p.x, grad_dtype=torch.float32, **p.rows())
+        h[60, 3], p.x[60, 7] = float("nan"), float("inf")
+        p.s[1] = float("inf")
+        got = g.lora_backward(dy, h, p.A, p.B, p.offsets, x=p.x, grad_dtype=torch.float32, **p.rows())
+        for u, v in zip(got[1:], clean[1:]):
+            assert torch.equal(u[[0, 2]], v[[0, 2]])
+        assert not torch.isfinite(got[2][1, :, 3]).any() and not torch.isfinite(got[1][1, :, 7]).any()
+
+
 def test_other_stream():
     g = lib()
     p = Problem([9, 0, 300], 32, 512, 640)
