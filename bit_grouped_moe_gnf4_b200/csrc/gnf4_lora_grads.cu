@@ -359,14 +359,14 @@ cudaError_t launch_grads_r(const LoraGradArgs& a, bool f32, cudaStream_t s) {
     int cs = 1;
     while (cs < 8 && wide * cs * 2 <= room && avg >= 128 * 2 * cs) cs *= 2;
     if (2 * wide * cs >= room || narrow > sms) {
-        if (cs > 1 || avg < 32) return launch_grads_w<RP, 1>(a, f32, cs, s);
+        LoraGradArgs b = a;
+        b.heavy = cs > 1 ? 0 : heavy_rows(a.R, avg);
+        if (b.heavy == 0) return launch_grads_w<RP, 1>(a, f32, cs, s);
         // One CTA an item: adapters of four times the average's rows get a cluster. us of a backward
         // pass at 2048 and 1536 columns, without and with it, the routing uniform and then with shares
         // like 1 / e: 128 adapters, 32768 rows, rank 16 126 to 135 and 257 to 141; 64 adapters, 4096
         // rows 34 to 37 and 50 to 37; at 10 rows an adapter (rank 32) 46 to 50 and 51 to 52.
         // Clusters of 2 leave that 257 at 177, of 8 at 152.
-        LoraGradArgs b = a;
-        b.heavy = (int)(4 * avg > 256 ? 4 * avg : 256);
         return launch_grads_w<RP, 1>(b, f32, 4, s);
     }
     cs = 1;

@@ -118,6 +118,13 @@ cudaError_t launch_grads_kernel(const LoraGradArgs& a, int cols, int cs, int sme
     return cudaLaunchKernelEx(&cfg, KERNEL, a);
 }
 
+// The rows from which an adapter is heavy, four times the average's and 256 at least; 0 if there
+// are too few rows for one to be, or for the search (2.5 us) to pay.
+inline int heavy_rows(int64_t R, int64_t avg) {
+    const int64_t heavy = 4 * avg > 256 ? 4 * avg : 256;
+    return avg < 32 || heavy >= R ? 0 : (int)heavy;
+}
+
 // ranks above 32 (gnf4_lora_grads_wide.cu)
 cudaError_t launch_lora_grads_wide(const LoraGradArgs& a, bool f32, cudaStream_t s);
 

@@ -392,10 +392,9 @@ cudaError_t launch_wide_r(const LoraGradArgs& a, bool f32, cudaStream_t s) {
     const int64_t items = active * (grad_items(a.a, CW) + grad_items(a.b, CW));
     int cs = 1;
     while (cs < 8 && items * cs * 2 <= room && avg >= 128 * 2 * cs) cs *= 2;
-    if (cs > 1 || avg < 32) return launch_wide_w<RP>(a, f32, cs, s);
     LoraGradArgs b = a;
-    b.heavy = (int)(4 * avg > 256 ? 4 * avg : 256);
-    return launch_wide_w<RP>(b, f32, 2, s);
+    b.heavy = cs > 1 ? 0 : heavy_rows(a.R, avg);
+    return launch_wide_w<RP>(b, f32, b.heavy ? 2 : cs, s);
 }
 
 }  // namespace
