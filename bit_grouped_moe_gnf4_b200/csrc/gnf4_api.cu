@@ -733,6 +733,7 @@ gnf4_status gnf4_lora_apply(const void* base, const void* x, int dtype, const vo
     if (st != GNF4_OK || R == 0) return st;
     if ((st = check_lora_buffers(c)) != GNF4_OK) return st;
     if (!x || !out) return fail(GNF4_ERR_INVALID_ARG, "null pointer argument");
+    if (T_in < 1) return fail(GNF4_ERR_INVALID_ARG, "x must have a row (a token out of range is read as one and left out)");
     if (out == x) return fail(GNF4_ERR_INVALID_ARG, "out may be base, but not x");
     if (!aligned16(x) || !aligned16(base) || !aligned16(out) || !aligned16(h))
         return fail(GNF4_ERR_MISALIGNED, "x, base, out and h must be 16-byte aligned");
@@ -778,6 +779,7 @@ gnf4_status gnf4_lora_backward(const void* grad_out, const void* x, const int8_t
     if (R > 0) {
         if ((st = check_lora_buffers(c)) != GNF4_OK) return st;
         if (!grad_out || !h || !grad_h || (dx_base && !dx)) return fail(GNF4_ERR_INVALID_ARG, "null pointer argument");
+        if (T_g < 1) return fail(GNF4_ERR_INVALID_ARG, "grad_out must have a row (a source out of range is read as one and left out)");
         if (grad_h == h || dx == grad_out) return fail(GNF4_ERR_INVALID_ARG, "grad_h may not be h, nor dx grad_out");
         if ((st = check_lora_x(x, x_codes, x_scales, !dA)) != GNF4_OK) return st;
     } else if (!adapter_offsets || !aligned8(adapter_offsets)) {

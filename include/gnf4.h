@@ -439,7 +439,7 @@ gnf4_status gnf4_swiglu_backward(const void* grad_out, const void* gate_up, cons
  * 2^30. 16-bit buffers and h are 16-byte aligned, row arrays and scaling 4-byte, offsets 8-byte.
  * Sums in fp32; h enters the second product with about 17 significant bits (two 16-bit terms).
  * Deterministic: the same call gives the same bits. R == 0 launches nothing and accepts NULL
- * buffers.
+ * buffers; with R > 0, T_in (the backward's T_g) is at least 1.
  * flags: 0 or GNF4_CHECK (validates offsets, row arrays and weights on the device first: one
  * extra kernel and a stream sync).
  * Errors: INVALID_ARG, UNSUPPORTED_SHAPE, MISALIGNED, DEVICE_STATUS (GNF4_CHECK), CUDA.

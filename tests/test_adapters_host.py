@@ -87,6 +87,13 @@ def test_grad_a_refusals(kw, status):
     assert lib.gnf4_last_error()
 
 
+def test_rows_of_an_empty_tensor_are_refused():
+    # every row's index is then out of range, and an address to read in its place is missing
+    assert apply(T_in=0, tok=FAKE) == INVALID and b"must have a row" in lib.gnf4_last_error()
+    assert backward(T_g=0, src=FAKE) == INVALID and b"must have a row" in lib.gnf4_last_error()
+    assert apply(T_in=0, tok=FAKE, R=0) == OK
+
+
 def test_act8_refusals():
     q, d = lib.gnf4_quantize_act8, lib.gnf4_dequantize_act8
     for f in (lambda a, r, K, b, c: q(a, r, K, b, c, None), lambda a, r, K, b, c: d(b, c, r, K, a, None)):
