@@ -10,7 +10,8 @@
 // What bounds it is instruction issue: about 330 instructions a warp and stage of 32 rows (the
 // copies' addresses, the split of left, the products; 450 with codes), issue slots 47 % busy
 // and a third of the stalls on loads, with DRAM at a fifth of its rate. 128 experts over 32768
-// rows, rank 16, 2048 checkpointed and 1536 columns: 64 us. Warps that only copy beside warps
+// rows, rank 16, 2048 checkpointed and 1536 columns: 64 us, and 72 with the search for heavy
+// adapters and whole clusters (see the rule below). Warps that only copy beside warps
 // that only multiply took 65 to 75 us there, with bulk copies of a row (52 to 67 cycles each
 // from one CTA) or 16-byte ones.
 #include <cstdint>

@@ -14,10 +14,12 @@
 // columns, 64 adapters, 8192 rows, a backward pass of 87 us instead of 118; one adapter of 4096
 // rows 50 and 71; rank 128, 100 adapters, 4096 rows 229 and 258. At rank 16 their fragments are
 // few, and the parts that stay (a CTA's start, the split of left, the last sum) cost more than
-// they do: 155 and 135 us with 128 adapters, 32768 rows, so that ranks up to 32 keep them. What
-// bounds it there is issue: 54 M instructions, the tensor pipe at 14 %. Persistent CTAs whose
-// copies run on into the next item: 84 us instead of 87 above, but 103 and not 90 with shares
-// like 1 / e, and 145 and not 137 at rank 128 (64 adapters, 8192 rows, 1024 columns).
+// they do: 155 and 135 us with 128 adapters, 32768 rows, so that ranks up to 32 keep them.
+// What bounds it is the chain of a stage (copied, made, multiplied) and its issue: in the first
+// case 22 M instructions, 0.39 a cycle and scheduler, half of the stalls on shared memory and
+// barriers, the tensor pipe and DRAM at 8 %. Persistent CTAs whose copies run on into the next
+// item: 84 us instead of 87 there, but 103 and not 90 with shares like 1 / e, and 145 and not
+// 137 at rank 128 (64 adapters, 8192 rows, 1024 columns).
 #include <cstdint>
 #include <cuda_runtime.h>
 
