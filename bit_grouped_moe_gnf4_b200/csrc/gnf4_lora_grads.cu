@@ -10,8 +10,7 @@
 // What bounds it is instruction issue: about 330 instructions a warp and stage of 32 rows (the
 // copies' addresses, the split of left, the products; 450 with codes), issue slots 47 % busy
 // and a third of the stalls on loads, with DRAM at a fifth of its rate. 128 experts over 32768
-// rows, rank 16, 2048 checkpointed and 1536 columns: 64 us, and 72 with the search for heavy
-// adapters and whole clusters (see the rule below). Warps that only copy beside warps
+// rows, rank 16, 2048 checkpointed and 1536 columns: 64 us. Warps that only copy beside warps
 // that only multiply took 65 to 75 us there, with bulk copies of a row (52 to 67 cycles each
 // from one CTA) or 16-byte ones.
 #include <cstdint>
@@ -325,7 +324,8 @@ __global__ void __launch_bounds__(kLoraThreads, WR == 1 ? 2 : 1) lora_grads_kern
         if (it.side_b) grad_body<RP, WR, TERMS, false>(p, p.b, it, smem);
         else grad_body<RP, WR, TERMS, Q8>(p, p.a, it, smem);
     }
-    if (threadIdx.x == 0) wait_for_previous_grid();      // whoever waits for this grid waits for that one too
+    // whoever waits for this grid waits for that one too; a CTA without an item leaves its place at once
+    if (threadIdx.x == 0 && (it.e < p.L || blockIdx.x == 0)) wait_for_previous_grid();
 }
 
 template <int RP, int WR, int TERMS, bool Q8>
@@ -363,11 +363,9 @@ cudaError_t launch_grads_r(const LoraGradArgs& a, bool f32, cudaStream_t s) {
         LoraGradArgs b = a;
         b.heavy = cs > 1 ? 0 : heavy_rows(a.R, avg);
         if (b.heavy == 0) return launch_grads_w<RP, 1>(a, f32, cs, s);
-        // One CTA an item: adapters of four times the average's rows get a cluster. us of a backward
-        // pass at 2048 and 1536 columns, without and with it, the routing uniform and then with shares
-        // like 1 / e: 128 adapters, 32768 rows, rank 16 126 to 135 and 257 to 141; 64 adapters, 4096
-        // rows 34 to 37 and 50 to 37; at 10 rows an adapter (rank 32) 46 to 50 and 51 to 52.
-        // Clusters of 2 leave that 257 at 177, of 8 at 152.
+        // One CTA an item, and clusters for the heavy adapters. us of a backward pass at 2048 and 1536
+        // columns, 128 adapters, 32768 rows, rank 16, without and with them: even rows 123 and 125,
+        // shares like 1 / e 342 and 155 (203 with clusters of 2).
         return launch_grads_w<RP, 1>(b, f32, 4, s);
     }
     cs = 1;

@@ -365,7 +365,8 @@ __global__ void __launch_bounds__(kLoraThreads, 2) lora_grads_wide_kernel(const 
     __syncthreads();
     tc_after();
     if (threadIdx.x < 32) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(ctl->tmem), "n"(CW));
-    if (threadIdx.x == 0) wait_for_previous_grid();      // whoever waits for this grid waits for that one too
+    // whoever waits for this grid waits for that one too; a CTA without an item leaves its place at once
+    if (threadIdx.x == 0 && (it.e < p.L || blockIdx.x == 0)) wait_for_previous_grid();
 }
 
 template <int RP, int TERMS, bool Q8>
