@@ -12,7 +12,6 @@
 // neighbouring lanes hold one block of 32, so a block's scale is two shuffles. They are
 // bound by HBM: the arithmetic is about 4 instructions an element for the codes and 15 for
 // the SwiGLU's gradients.
-#include <climits>
 #include <cstdint>
 #include <cuda_runtime.h>
 
@@ -23,10 +22,10 @@ namespace gnf4 {
 
 namespace {
 
-// small CTAs, as many as the data has (a grid of a few CTAs an SM that strides over it was 2 to
-// 14 % slower: 41 us against 36 for the codes of 32768 x 2048, 42 against 39 for the SwiGLU)
+// small CTAs, as many as the data has, one pass each (a grid of a few CTAs an SM that strides over it
+// was 2 to 14 % slower: 41 us against 36 for the codes of 32768 x 2048, 42 against 39 for the SwiGLU)
 constexpr int kActThreads = 128;
-constexpr int kActVecs = 4;            // 16-byte vectors per thread and pass (loads issued together)
+constexpr int kActVecs = 4;            // 16-byte vectors per thread (loads issued together)
 constexpr int kSwigluActVecs = 2;      // the SwiGLU kernels hold three or four arrays per vector
 
 __device__ __forceinline__ float lo_f(uint32_t w) { return __uint_as_float(w << 16); }
@@ -92,7 +91,7 @@ __device__ __forceinline__ uint4 decode8(const uint2& q, uint32_t s) {
                       act8_pair(prmt(q.y, 0u, 0x0100u), step), act8_pair(prmt(q.y, 0u, 0x0302u), step));
 }
 
-// r = i / d for the 32-bit walks: a multiplication and two shifts (the round-up method of Granlund
+// r = i / d in 32 bits: a multiplication and two shifts (the round-up method of Granlund
 // and Montgomery, 1994)
 struct Divider {
     uint32_t d, m, s;
@@ -106,23 +105,20 @@ struct Divider {
 // total: 16-byte vectors; a multiple of 4, so the four lanes of a block are all in range or all out
 __global__ void __launch_bounds__(kActThreads) quantize_act8_kernel(const uint4* __restrict__ x, uint2* __restrict__ codes,
                                                                     uint8_t* __restrict__ scales, int64_t total) {
-    const int64_t stride = (int64_t)gridDim.x * (kActThreads * kActVecs);
-    for (int64_t b = (int64_t)blockIdx.x * (kActThreads * kActVecs); b < total; b += stride) {
-        const int64_t base = b + threadIdx.x;
-        uint4 v[kActVecs];
+    const int64_t base = (int64_t)blockIdx.x * (kActThreads * kActVecs) + threadIdx.x;
+    uint4 v[kActVecs];
 #pragma unroll
-        for (int j = 0; j < kActVecs; ++j) {
-            const int64_t i = base + j * kActThreads;
-            v[j] = i < total ? __ldg(x + i) : make_uint4(0u, 0u, 0u, 0u);
-        }
+    for (int j = 0; j < kActVecs; ++j) {
+        const int64_t i = base + j * kActThreads;
+        v[j] = i < total ? __ldg(x + i) : make_uint4(0u, 0u, 0u, 0u);
+    }
 #pragma unroll
-        for (int j = 0; j < kActVecs; ++j) {
-            const int64_t i = base + j * kActThreads;
-            const uint32_t s = block_scale(v[j]);
-            if (i < total) {
-                codes[i] = encode8(v[j], s);
-                if ((i & 3) == 0) scales[i >> 2] = (uint8_t)s;
-            }
+    for (int j = 0; j < kActVecs; ++j) {
+        const int64_t i = base + j * kActThreads;
+        const uint32_t s = block_scale(v[j]);
+        if (i < total) {
+            codes[i] = encode8(v[j], s);
+            if ((i & 3) == 0) scales[i >> 2] = (uint8_t)s;
         }
     }
 }
@@ -130,23 +126,21 @@ __global__ void __launch_bounds__(kActThreads) quantize_act8_kernel(const uint4*
 __global__ void __launch_bounds__(kActThreads) dequantize_act8_kernel(const uint2* __restrict__ codes,
                                                                       const uint8_t* __restrict__ scales,
                                                                       uint4* __restrict__ out, int64_t total) {
-    const int64_t stride = (int64_t)gridDim.x * (kActThreads * kActVecs);
-    for (int64_t base = (int64_t)blockIdx.x * (kActThreads * kActVecs) + threadIdx.x; base < total; base += stride) {
-        uint2 q[kActVecs];
-        uint32_t s[kActVecs];
+    const int64_t base = (int64_t)blockIdx.x * (kActThreads * kActVecs) + threadIdx.x;
+    uint2 q[kActVecs];
+    uint32_t s[kActVecs];
 #pragma unroll
-        for (int j = 0; j < kActVecs; ++j) {
-            const int64_t i = base + j * kActThreads;
-            if (i < total) {
-                q[j] = __ldg(codes + i);
-                s[j] = __ldg(scales + (i >> 2));
-            }
+    for (int j = 0; j < kActVecs; ++j) {
+        const int64_t i = base + j * kActThreads;
+        if (i < total) {
+            q[j] = __ldg(codes + i);
+            s[j] = __ldg(scales + (i >> 2));
         }
+    }
 #pragma unroll
-        for (int j = 0; j < kActVecs; ++j) {
-            const int64_t i = base + j * kActThreads;
-            if (i < total) out[i] = decode8(q[j], s[j]);
-        }
+    for (int j = 0; j < kActVecs; ++j) {
+        const int64_t i = base + j * kActThreads;
+        if (i < total) out[i] = decode8(q[j], s[j]);
     }
 }
 
@@ -161,35 +155,33 @@ __global__ void __launch_bounds__(kActThreads) swiglu_act8_kernel(const uint4* _
                                                                   uint2* __restrict__ codes,
                                                                   uint8_t* __restrict__ scales, Divider by, IDX total) {
     const IDX I8 = (IDX)by.d;
-    const IDX stride = (IDX)gridDim.x * (kActThreads * kSwigluActVecs);
-    for (IDX b = (IDX)blockIdx.x * (kActThreads * kSwigluActVecs); b < total; b += stride) {
-        uint4 g[kSwigluActVecs], u[kSwigluActVecs];
-        int64_t at[kSwigluActVecs];              // vector index of the gate in the [R, 2I] rows
+    const IDX base = (IDX)blockIdx.x * (kActThreads * kSwigluActVecs) + threadIdx.x;
+    uint4 g[kSwigluActVecs], u[kSwigluActVecs];
+    int64_t at[kSwigluActVecs];              // vector index of the gate in the [R, 2I] rows
 #pragma unroll
-        for (int j = 0; j < kSwigluActVecs; ++j) {
-            const IDX i = b + threadIdx.x + (IDX)j * kActThreads;
-            g[j] = u[j] = make_uint4(0u, 0u, 0u, 0u);
-            at[j] = 0;
-            if (i < total) {
-                const IDX r = by(i);
-                at[j] = (int64_t)i + (int64_t)r * I8;      // r * 2 I8 + (i - r I8)
-                g[j] = __ldg(h + at[j]);
-                u[j] = __ldg(h + at[j] + I8);
-            }
+    for (int j = 0; j < kSwigluActVecs; ++j) {
+        const IDX i = base + (IDX)j * kActThreads;
+        g[j] = u[j] = make_uint4(0u, 0u, 0u, 0u);
+        at[j] = 0;
+        if (i < total) {
+            const IDX r = by(i);
+            at[j] = (int64_t)i + (int64_t)r * I8;      // r * 2 I8 + (i - r I8)
+            g[j] = __ldg(h + at[j]);
+            u[j] = __ldg(h + at[j] + I8);
         }
+    }
 #pragma unroll
-        for (int j = 0; j < kSwigluActVecs; ++j) {
-            const IDX i = b + threadIdx.x + (IDX)j * kActThreads;
-            const uint32_t sg = block_scale(g[j]), su = block_scale(u[j]);
-            if (i < total) {
-                out[i] = make_uint4(silu_word(g[j].x, u[j].x), silu_word(g[j].y, u[j].y),
-                                    silu_word(g[j].z, u[j].z), silu_word(g[j].w, u[j].w));
-                codes[at[j]] = encode8(g[j], sg);
-                codes[at[j] + I8] = encode8(u[j], su);
-                if ((i & 3) == 0) {
-                    scales[at[j] >> 2] = (uint8_t)sg;
-                    scales[(at[j] + I8) >> 2] = (uint8_t)su;
-                }
+    for (int j = 0; j < kSwigluActVecs; ++j) {
+        const IDX i = base + (IDX)j * kActThreads;
+        const uint32_t sg = block_scale(g[j]), su = block_scale(u[j]);
+        if (i < total) {
+            out[i] = make_uint4(silu_word(g[j].x, u[j].x), silu_word(g[j].y, u[j].y),
+                                silu_word(g[j].z, u[j].z), silu_word(g[j].w, u[j].w));
+            codes[at[j]] = encode8(g[j], sg);
+            codes[at[j] + I8] = encode8(u[j], su);
+            if ((i & 3) == 0) {
+                scales[at[j] >> 2] = (uint8_t)sg;
+                scales[(at[j] + I8) >> 2] = (uint8_t)su;
             }
         }
     }
@@ -228,58 +220,56 @@ __global__ void __launch_bounds__(kActThreads) swiglu_backward_kernel(const uint
                                                                       uint4* __restrict__ dh, uint4* __restrict__ again,
                                                                       Divider by, IDX total) {
     const IDX I8 = (IDX)by.d;
-    const IDX stride = (IDX)gridDim.x * (kActThreads * kSwigluActVecs);
-    for (IDX base = (IDX)blockIdx.x * (kActThreads * kSwigluActVecs) + threadIdx.x; base < total; base += stride) {
-        uint4 g[kSwigluActVecs], u[kSwigluActVecs], dv[kSwigluActVecs];
-        uint2 qg[kSwigluActVecs], qu[kSwigluActVecs];
-        uint32_t sg[kSwigluActVecs], su[kSwigluActVecs];
-        int64_t at[kSwigluActVecs];
+    const IDX base = (IDX)blockIdx.x * (kActThreads * kSwigluActVecs) + threadIdx.x;
+    uint4 g[kSwigluActVecs], u[kSwigluActVecs], dv[kSwigluActVecs];
+    uint2 qg[kSwigluActVecs], qu[kSwigluActVecs];
+    uint32_t sg[kSwigluActVecs], su[kSwigluActVecs];
+    int64_t at[kSwigluActVecs];
 #pragma unroll
-        for (int j = 0; j < kSwigluActVecs; ++j) {
-            const IDX i = base + (IDX)j * kActThreads;
-            if (i < total) {
-                const IDX r = by(i);
-                at[j] = (int64_t)i + (int64_t)r * I8;
-                dv[j] = __ldg(d + i);
-                if (Q8) {
-                    qg[j] = __ldg(codes + at[j]);
-                    qu[j] = __ldg(codes + at[j] + I8);
-                    sg[j] = __ldg(scales + (at[j] >> 2));
-                    su[j] = __ldg(scales + ((at[j] + I8) >> 2));
-                } else {
-                    g[j] = __ldg(h + at[j]);
-                    u[j] = __ldg(h + at[j] + I8);
-                }
+    for (int j = 0; j < kSwigluActVecs; ++j) {
+        const IDX i = base + (IDX)j * kActThreads;
+        if (i < total) {
+            const IDX r = by(i);
+            at[j] = (int64_t)i + (int64_t)r * I8;
+            dv[j] = __ldg(d + i);
+            if (Q8) {
+                qg[j] = __ldg(codes + at[j]);
+                qu[j] = __ldg(codes + at[j] + I8);
+                sg[j] = __ldg(scales + (at[j] >> 2));
+                su[j] = __ldg(scales + ((at[j] + I8) >> 2));
+            } else {
+                g[j] = __ldg(h + at[j]);
+                u[j] = __ldg(h + at[j] + I8);
             }
         }
+    }
 #pragma unroll
-        for (int j = 0; j < kSwigluActVecs; ++j) {
-            const IDX i = base + (IDX)j * kActThreads;
-            if (i < total) {
-                if (Q8) {
-                    g[j] = decode8(qg[j], sg[j]);
-                    u[j] = decode8(qu[j], su[j]);
-                }
-                uint4 dg, du, act;
-                swiglu_grad_word(g[j].x, u[j].x, dv[j].x, dg.x, du.x, act.x);
-                swiglu_grad_word(g[j].y, u[j].y, dv[j].y, dg.y, du.y, act.y);
-                swiglu_grad_word(g[j].z, u[j].z, dv[j].z, dg.z, du.z, act.z);
-                swiglu_grad_word(g[j].w, u[j].w, dv[j].w, dg.w, du.w, act.w);
-                dh[at[j]] = dg;
-                dh[at[j] + I8] = du;
-                if (again) again[i] = act;
+    for (int j = 0; j < kSwigluActVecs; ++j) {
+        const IDX i = base + (IDX)j * kActThreads;
+        if (i < total) {
+            if (Q8) {
+                g[j] = decode8(qg[j], sg[j]);
+                u[j] = decode8(qu[j], su[j]);
             }
+            uint4 dg, du, act;
+            swiglu_grad_word(g[j].x, u[j].x, dv[j].x, dg.x, du.x, act.x);
+            swiglu_grad_word(g[j].y, u[j].y, dv[j].y, dg.y, du.y, act.y);
+            swiglu_grad_word(g[j].z, u[j].z, dv[j].z, dg.z, du.z, act.z);
+            swiglu_grad_word(g[j].w, u[j].w, dv[j].w, dg.w, du.w, act.w);
+            dh[at[j]] = dg;
+            dh[at[j] + I8] = du;
+            if (again) again[i] = act;
         }
     }
 }
 
+// the sizes that are let in (2^41 elements) make 2^30 CTAs at most
 int act_grid(int64_t total, int per_thread) {
     const int64_t per_cta = (int64_t)kActThreads * per_thread;
-    const int64_t want = (total + per_cta - 1) / per_cta;
-    return (int)(want < INT_MAX ? want : INT_MAX);
+    return (int)((total + per_cta - 1) / per_cta);
 }
 
-// I8 vectors a row, 1 < I8 < 2^31 (1 has no shift of its own: the 64-bit walk takes it)
+// I8 vectors a row, 1 < I8 < 2^31 (1 has no shift of its own: the 64-bit kernels take it)
 Divider divider(int64_t I8) {
     Divider v{(uint32_t)I8, 0u, 0u};
     int l = 0;
@@ -291,9 +281,9 @@ Divider divider(int64_t I8) {
     return v;
 }
 
-// whether every index a 32-bit walk over `total` vectors forms fits in 32 bits
-bool fits_u32(int64_t total, int grid, int per_thread, int64_t I8) {
-    return total <= (int64_t)UINT32_MAX - 2 * (int64_t)grid * kActThreads * per_thread && I8 > 1;
+// whether every index that the CTAs of `total` vectors form fits in 32 bits
+bool fits_u32(int64_t total, int64_t I8) {
+    return total <= (int64_t)UINT32_MAX - kActThreads * kSwigluActVecs && I8 > 1;
 }
 
 }  // namespace
@@ -319,7 +309,7 @@ cudaError_t launch_swiglu_act8(const void* gate_up, int64_t R, int64_t I, void* 
     const uint4* h = reinterpret_cast<const uint4*>(gate_up);
     uint4* o = reinterpret_cast<uint4*>(out);
     uint2* q = reinterpret_cast<uint2*>(codes);
-    if (fits_u32(total, grid, kSwigluActVecs, I8))
+    if (fits_u32(total, I8))
         swiglu_act8_kernel<uint32_t><<<grid, kActThreads, 0, s>>>(h, o, q, scales, divider(I8), (uint32_t)total);
     else
         swiglu_act8_kernel<int64_t><<<grid, kActThreads, 0, s>>>(h, o, q, scales, divider(I8), total);
@@ -335,7 +325,7 @@ cudaError_t launch_swiglu_backward(const void* d_out, const void* gate_up, const
     const uint2* q = reinterpret_cast<const uint2*>(codes);
     uint4* dh = reinterpret_cast<uint4*>(d_gate_up);
     uint4* a = reinterpret_cast<uint4*>(again);
-    const bool small = fits_u32(total, grid, kSwigluActVecs, I8);
+    const bool small = fits_u32(total, I8);
     if (gate_up && small)
         swiglu_backward_kernel<uint32_t, false><<<grid, kActThreads, 0, s>>>(d, h, q, scales, dh, a, divider(I8), (uint32_t)total);
     else if (gate_up)

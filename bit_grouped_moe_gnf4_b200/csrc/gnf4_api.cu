@@ -394,19 +394,21 @@ static gnf4_status check_act8_args(const void* x16, const void* codes, const voi
     return check_device({x16, codes, scales});
 }
 
+constexpr int64_t kMostActElements = (int64_t)1 << 41;    // a grid's CTAs, of 2048 elements at least, stay below 2^31
+
 // sizes of an [rows, K] checkpoint
 static gnf4_status check_act8_sizes(int64_t rows, int64_t K) {
     if (rows < 0 || K < 1) return fail(GNF4_ERR_INVALID_ARG, "sizes must be rows >= 0 and K >= 1");
     if (K % 32) return fail(GNF4_ERR_UNSUPPORTED_SHAPE, "K must be a multiple of 32");
-    if (rows > INT64_MAX / 2 / K) return fail(GNF4_ERR_UNSUPPORTED_SHAPE, "rows * K must fit in int64");
+    if (rows > kMostActElements / K) return fail(GNF4_ERR_UNSUPPORTED_SHAPE, "rows * K must be at most 2^41");
     return GNF4_OK;
 }
 
 static gnf4_status check_swiglu_sizes(int64_t R, int64_t I, int64_t imul) {
     if (R < 0 || I < 1) return fail(GNF4_ERR_INVALID_ARG, "sizes must be R >= 0 and I >= 1");
     if (I % imul) return fail(GNF4_ERR_UNSUPPORTED_SHAPE, "I must be a multiple of %lld", (long long)imul);
-    if (I > (1 << 30) || R > INT64_MAX / 4 / I)
-        return fail(GNF4_ERR_UNSUPPORTED_SHAPE, "I must be at most 2^30 and R * 2I fit in int64");
+    if (I > (1 << 30) || R > kMostActElements / I)
+        return fail(GNF4_ERR_UNSUPPORTED_SHAPE, "I must be at most 2^30 and R * I at most 2^41");
     return GNF4_OK;
 }
 

@@ -370,9 +370,9 @@ gnf4_status gnf4_combine_topk(const void* y, int64_t R, int64_t N, const int32_t
  * x, out device bf16 [rows, K], 16-byte aligned
  * codes  device int8  [rows, K], 16-byte aligned
  * scales device uint8 [rows, K/32]
- * rows >= 0, K % 32 == 0. One kernel launch; rows == 0 launches nothing and accepts NULL
- * buffers. Outputs may not overlap inputs.
- * Errors: INVALID_ARG (null/host pointer, rows < 0, K < 1), UNSUPPORTED_SHAPE (K % 32), MISALIGNED.
+ * rows >= 0, K % 32 == 0, rows * K at most 2^41. One kernel launch; rows == 0 launches nothing and
+ * accepts NULL buffers. Outputs may not overlap inputs.
+ * Errors: INVALID_ARG (null/host pointer, rows < 0, K < 1), UNSUPPORTED_SHAPE, MISALIGNED.
  */
 gnf4_status gnf4_quantize_act8(const void* x, int64_t rows, int64_t K, int8_t* codes, uint8_t* scales,
                                void* stream);
@@ -383,8 +383,8 @@ gnf4_status gnf4_dequantize_act8(const int8_t* codes, const uint8_t* scales, int
  * gnf4_swiglu that also writes the checkpoint of its gate_up rows, in one pass over them:
  * out is gnf4_swiglu's bit for bit, codes and scales are gnf4_quantize_act8's of gate_up.
  * gate_up device bf16 [R, 2I], 16-byte aligned; out device bf16 [R, I], 16-byte aligned;
- * codes device int8 [R, 2I], 16-byte aligned; scales device uint8 [R, 2I/32]. I % 32 == 0, I <= 2^30.
- * One kernel launch; R == 0 launches nothing and accepts NULL buffers.
+ * codes device int8 [R, 2I], 16-byte aligned; scales device uint8 [R, 2I/32]. I % 32 == 0, I <= 2^30,
+ * R * I at most 2^41. One kernel launch; R == 0 launches nothing and accepts NULL buffers.
  */
 gnf4_status gnf4_swiglu_act8(const void* gate_up, int64_t R, int64_t I, void* out, int8_t* codes,
                              uint8_t* scales, void* stream);
@@ -402,8 +402,8 @@ gnf4_status gnf4_swiglu_act8(const void* gate_up, int64_t R, int64_t I, void* ou
  * grad_out device bf16 [R, I]; gate_up device bf16 [R, 2I] or NULL; codes device int8 [R, 2I]
  * (16-byte aligned) and scales device uint8 [R, 2I/32], given exactly if gate_up is not;
  * grad_gate_up device bf16 [R, 2I]; act device bf16 [R, I] or NULL. bf16 buffers are 16-byte
- * aligned; outputs may not overlap inputs. I % 8 == 0 (I % 32 == 0 with a checkpoint), I <= 2^30.
- * One kernel launch; R == 0 launches nothing and accepts NULL buffers.
+ * aligned; outputs may not overlap inputs. I % 8 == 0 (I % 32 == 0 with a checkpoint), I <= 2^30,
+ * R * I at most 2^41. One kernel launch; R == 0 launches nothing and accepts NULL buffers.
  * Errors: INVALID_ARG, UNSUPPORTED_SHAPE, MISALIGNED.
  */
 gnf4_status gnf4_swiglu_backward(const void* grad_out, const void* gate_up, const int8_t* codes,

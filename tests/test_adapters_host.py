@@ -114,6 +114,21 @@ def test_act8_refusals():
     assert b"device memory" in lib.gnf4_last_error()
 
 
+def test_sizes_past_one_pass_of_a_grid_are_refused():
+    # 2^41 elements are let in (and then refused as no device memory); there is no second pass beyond
+    most = 1 << 41
+    for rows, K in ((1, most), (1 << 20, 1 << 21), (1 << 36, 32)):
+        assert lib.gnf4_quantize_act8(FAKE, rows, K, FAKE, FAKE, None) == INVALID
+        assert lib.gnf4_quantize_act8(FAKE, rows + 1, K, FAKE, FAKE, None) == SHAPE
+        assert lib.gnf4_dequantize_act8(FAKE, FAKE, rows + 1, K, FAKE, None) == SHAPE
+        assert b"2^41" in lib.gnf4_last_error()
+    for R, I in ((1 << 20, 1 << 21), (1 << 36, 32), (1 << 11, 1 << 30)):
+        assert lib.gnf4_swiglu_act8(FAKE, R, I, FAKE, FAKE, FAKE, None) == INVALID
+        assert lib.gnf4_swiglu_act8(FAKE, R + 1, I, FAKE, FAKE, FAKE, None) == SHAPE
+        assert lib.gnf4_swiglu_backward(FAKE, FAKE, None, None, R + 1, I, FAKE, None, None) == SHAPE
+    assert lib.gnf4_swiglu_backward(FAKE, FAKE, None, None, 1 << 39, 8, FAKE, None, None) == SHAPE
+
+
 def test_swiglu_refusals():
     f = lib.gnf4_swiglu_act8
     assert f(FAKE, 4, 40, FAKE, FAKE, FAKE, None) == SHAPE
