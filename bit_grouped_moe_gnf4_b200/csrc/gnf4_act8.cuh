@@ -8,22 +8,7 @@
 
 namespace gnf4 {
 
-// one step of a block, 2^(s-133): an fp32 subnormal for s < 7, NaN for s = 255
-__device__ __forceinline__ float act8_step(uint32_t s) {
-    if (s == 255u) return __uint_as_float(0x7FC00000u);
-    return __uint_as_float(s >= 7u ? (s - 6u) << 23 : 1u << (s + 16u));
-}
-
-// The values of 8 codes, exact: 128 + c is placed in the low mantissa byte of 2^23, and
-// 2^23 + 128 taken off again leaves c.
-__device__ __forceinline__ void act8_values(const uint2& q, float step, float (&f)[8]) {
-    const uint32_t u[2] = {q.x ^ 0x80808080u, q.y ^ 0x80808080u};
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-        f[i] = (__uint_as_float(prmt(u[i >> 2], 0x4B000000u, 0x7440u + (i & 3))) - 8388736.0f) * step;
-}
-
-// the step as a bf16 pattern (a subnormal for s < 7)
+// one step of a block, 2^(s-133), as a bf16 pattern: a subnormal for s < 7, NaN for s = 255
 __device__ __forceinline__ uint32_t act8_step_bf16(uint32_t s) {
     return s == 255u ? 0x7FC0u : s >= 7u ? (s - 6u) << 7 : 1u << s;
 }

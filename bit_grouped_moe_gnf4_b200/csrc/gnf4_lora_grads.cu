@@ -223,13 +223,9 @@ __device__ __forceinline__ void grad_body(const LoraGradArgs& p, const LoraGradS
                 for (int pair = 0; pair < 2; ++pair) {
                     const int row = r0 + 2 * t + 8 * pair;
                     const uint32_t at = x + (uint32_t)(row * S::kPitch8 + wc * S::SC + CT * g);
-                    uint32_t w[2][CT / 4];
-                    if constexpr (CT == 8) {
-                        const uint2 u = lds8(at), v = lds8(at + S::kPitch8);
-                        w[0][0] = u.x, w[0][1] = u.y, w[1][0] = v.x, w[1][1] = v.y;
-                    } else {
-                        w[0][0] = lds4(at), w[1][0] = lds4(at + S::kPitch8);
-                    }
+                    static_assert(CT == 8, "two words of codes a row");
+                    const uint2 u = lds8(at), v = lds8(at + S::kPitch8);
+                    const uint32_t w[2][CT / 4] = {{u.x, u.y}, {v.x, v.y}};
                     const uint16_t* st = s_step + (i & 1) * (S::scale_bytes / 2) + row * (CW / 32) + (wc * S::SC + CT * g) / 32;
                     const uint32_t step = (uint32_t)st[0] | (uint32_t)st[CW / 32] << 16;
 #pragma unroll

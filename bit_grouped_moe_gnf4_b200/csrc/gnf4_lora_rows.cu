@@ -13,7 +13,6 @@
 // operands, which leaves no copy through shared memory in that chain. One token with a rank
 // of 16, 2048 -> 2048: 5.5 us in a graph, launch included (8 CTAs share its 128 KB of
 // adapter; one by one they took 5.8); 61 tokens of 61 adapters 7.0 us, 7.9 MB: 1.1 TB/s.
-#include <atomic>
 #include <cstdint>
 #include <type_traits>
 #include <cuda_runtime.h>
