@@ -425,7 +425,8 @@ struct LoraCommon {
 static gnf4_status check_lora_sizes(const LoraCommon& c) {
     if (c.L < 1 || c.r < 1 || c.N < 1 || c.K < 1 || c.R < 0 || c.n_a < 0 || c.n_b < 0)
         return fail(GNF4_ERR_INVALID_ARG, "sizes must be L, r, N, K >= 1 and rows >= 0");
-    if (c.flags & ~GNF4_CHECK) return fail(GNF4_ERR_INVALID_ARG, "only GNF4_CHECK is accepted (flags 0x%x)", c.flags);
+    if (c.flags & ~(GNF4_CHECK | GNF4_TEST_STALL))
+        return fail(GNF4_ERR_INVALID_ARG, "only GNF4_CHECK and GNF4_TEST_STALL are accepted (flags 0x%x)", c.flags);
     if (c.r % 8 || c.r > 128) return fail(GNF4_ERR_UNSUPPORTED_SHAPE, "the rank must be a multiple of 8 up to 128");
     if (c.K % 8 || c.N % 8) return fail(GNF4_ERR_UNSUPPORTED_SHAPE, "K and N must be multiples of 8");
     if (c.L > 2048) return fail(GNF4_ERR_UNSUPPORTED_SHAPE, "at most 2048 adapters");
@@ -733,6 +734,8 @@ gnf4_status gnf4_lora_apply(const void* base, const void* x, int dtype, const vo
     const LoraCommon c{A, B, adapter_offsets, row_token, row_dest, row_weight, scaling, L, r, N, K, R, T_in, T_out, flags};
     gnf4_status st = check_lora_sizes(c);
     if (st != GNF4_OK || R == 0) return st;
+    if ((flags & GNF4_TEST_STALL) && r > 64)
+        return fail(GNF4_ERR_INVALID_ARG, "GNF4_TEST_STALL: nothing waits in lora_apply at ranks above 64");
     if ((st = check_lora_buffers(c)) != GNF4_OK) return st;
     if (!x || !out) return fail(GNF4_ERR_INVALID_ARG, "null pointer argument");
     if (T_in < 1) return fail(GNF4_ERR_INVALID_ARG, "x must have a row (a token out of range is read as one and left out)");
@@ -761,6 +764,7 @@ gnf4_status gnf4_lora_apply(const void* base, const void* x, int dtype, const vo
     a.r = (int)r;
     a.C = (int)K;
     a.O = (int)N;
+    a.test_stall = (flags & GNF4_TEST_STALL) ? 1 : 0;
     cudaError_t e = launch_lora_rows(a, false, dtype == GNF4_DTYPE_F16, s);
     return e == cudaSuccess ? GNF4_OK : cuda_fail(e, "lora_apply launch");
 }
@@ -814,6 +818,7 @@ gnf4_status gnf4_lora_backward(const void* grad_out, const void* x, const int8_t
         a.r = (int)r;
         a.C = (int)N;
         a.O = (int)K;
+        a.test_stall = (flags & GNF4_TEST_STALL) ? 1 : 0;
         cudaError_t e = launch_lora_rows(a, true, false, s);
         if (e != cudaSuccess) return cuda_fail(e, "lora_backward launch");
     }
@@ -837,6 +842,7 @@ gnf4_status gnf4_lora_backward(const void* grad_out, const void* x, const int8_t
     q.r = (int)r;
     q.heavy = 0;
     q.after_rows = R > 0;
+    q.test_stall = (flags & GNF4_TEST_STALL) ? 1 : 0;
     cudaError_t e = launch_lora_grads(q, grad_dtype == GNF4_DTYPE_F32, s);
     return e == cudaSuccess ? GNF4_OK : cuda_fail(e, "lora_backward gradient launch");
 }
@@ -850,6 +856,8 @@ gnf4_status gnf4_lora_grad_a(const float* grad_h, const void* x, const int8_t* x
     const LoraCommon c{nullptr, nullptr, adapter_offsets, row_token, nullptr, nullptr, nullptr, L, r, 8, K, R, T_in, R, flags};
     gnf4_status st = check_lora_sizes(c);
     if (st != GNF4_OK) return st;
+    if ((flags & GNF4_TEST_STALL) && r <= 32)
+        return fail(GNF4_ERR_INVALID_ARG, "GNF4_TEST_STALL: nothing waits in lora_grad_a at ranks up to 32");
     if (x_codes && K % 32) return fail(GNF4_ERR_UNSUPPORTED_SHAPE, "a checkpoint of x needs K % 32 == 0");
     if (!dA || !adapter_offsets || (R > 0 && !grad_h)) return fail(GNF4_ERR_INVALID_ARG, "null pointer argument");
     if (R > 0 && (st = check_lora_x(x, x_codes, x_scales, false)) != GNF4_OK) return st;
@@ -866,6 +874,7 @@ gnf4_status gnf4_lora_grad_a(const float* grad_h, const void* x, const int8_t* x
     q.R = R;
     q.L = (int)L;
     q.r = (int)r;
+    q.test_stall = (flags & GNF4_TEST_STALL) ? 1 : 0;
     cudaError_t e = launch_lora_grads(q, grad_dtype == GNF4_DTYPE_F32, s);
     return e == cudaSuccess ? GNF4_OK : cuda_fail(e, "lora_grad_a launch");
 }

@@ -84,6 +84,7 @@ struct LoraRowsArgs {
     float* mid;                 // [R, r] or null
     int64_t R, n_src, n_dst;
     int L, r, C, O;
+    int test_stall;             // testing: the streaming kernel copies nothing and waits at most 2^17 cycles
 };
 cudaError_t launch_lora_rows(const LoraRowsArgs& a, bool bwd, bool f16, cudaStream_t s);
 
@@ -108,6 +109,7 @@ struct LoraGradArgs {
     int L, r;
     int heavy;                  // set by the launch: more rows than this are shared by a cluster; 0: see the kernel
     int after_rows;             // a.left comes from the rows kernel launched just before on the stream
+    int test_stall;             // testing: ranks above 32 multiply nothing and wait at most 2^17 cycles
 };
 cudaError_t launch_lora_grads(const LoraGradArgs& a, bool f32, cudaStream_t s);
 cudaError_t launch_check_lora(const int64_t* offsets, int L, int64_t R, const int32_t* a, int64_t na, const int32_t* b,

@@ -33,6 +33,7 @@ namespace gnf4 {
 constexpr int kLoraThreads = 256;
 constexpr size_t kMaxSmem = 227 * 1024 - 512;      // dynamic shared memory of a CTA beside its static part
 constexpr int kLoraWarps = kLoraThreads / 32;
+constexpr long long kStallWaitCycles = 1LL << 17;   // where a test wants a wait to give up
 
 __device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
     uint32_t d;

@@ -219,7 +219,9 @@ __device__ __forceinline__ void grad_body(const LoraGradArgs& p, const LoraGradS
     const uint32_t tmem = ctl->tmem;
     bool gone = false;
     auto wait_made = [&](int i) {                        // the MMAs of stage i are through
-        if (!gone) gone = !mbar_wait_bounded(smem_addr(&ctl->done), (uint32_t)(i & 1), &ctl->abort, &g_grads_err, 1u);
+        if (!gone)
+            gone = !mbar_wait_bounded(smem_addr(&ctl->done), (uint32_t)(i & 1), &ctl->abort, &g_grads_err, 1u,
+                                      p.test_stall ? kStallWaitCycles : kWaitTimeoutCycles);
     };
     for (int i = 0; i < stages; ++i) {
         copy_wait<D - 1>();
@@ -244,7 +246,7 @@ __device__ __forceinline__ void grad_body(const LoraGradArgs& p, const LoraGradS
         }
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         __syncthreads();
-        if (tid == 0 && !gone) {
+        if (tid == 0 && !gone && !p.test_stall) {
             tc_after();
             const uint32_t a = made0;
             const uint32_t b = Q8 ? a + S::plane : stage0 + (uint32_t)(i % S::S * S::stage);

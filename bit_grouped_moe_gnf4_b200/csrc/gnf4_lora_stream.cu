@@ -132,6 +132,7 @@ __global__ void __launch_bounds__(StreamShape<RP, ROWS>::kThreads, 1) lora_strea
 
     if (warp >= kLoraWarps) {
         // ------------------------------------------------------------ producers
+        if (p.test_stall) return;                                    // no copies: the consumers' waits give up
         const int ptid = tid - kLoraThreads;
         int e = 0, row0 = 0, rows = 0;
         // the tile's adapter and rows, and the row index that this thread keeps for the tile: its
@@ -253,7 +254,8 @@ __global__ void __launch_bounds__(StreamShape<RP, ROWS>::kThreads, 1) lora_strea
     // ---------------------------------------------------------------- consumers
     auto wait_stage = [&]() {
         if (!gone)
-            gone = __any_sync(0xffffffffu, !mbar_wait_bounded(smem_addr(s_full + slot), phase, &s_abort, &g_lora_err, 2u));
+            gone = __any_sync(0xffffffffu, !mbar_wait_bounded(smem_addr(s_full + slot), phase, &s_abort, &g_lora_err, 2u,
+                                                              p.test_stall ? kStallWaitCycles : kWaitTimeoutCycles));
     };
     auto release_stage = [&]() {
         __syncwarp();

@@ -440,8 +440,10 @@ gnf4_status gnf4_swiglu_backward(const void* grad_out, const void* gate_up, cons
  * Sums in fp32; h enters the second product with about 17 significant bits (two 16-bit terms).
  * Deterministic: the same call gives the same bits. R == 0 launches nothing and accepts NULL
  * buffers; with R > 0, T_in (the backward's T_g) is at least 1.
- * flags: 0 or GNF4_CHECK (validates offsets, row arrays and weights on the device first: one
- * extra kernel and a stream sync).
+ * flags: GNF4_CHECK (validates offsets, row arrays and weights on the device first: one extra kernel
+ * and a stream sync) and GNF4_TEST_STALL (testing the error path as in the grouped call: the kernels
+ * that wait for copies, of any number of rows at ranks up to 64, and for matrix products, in the
+ * gradients of ranks above 32, start none and give up; a call without such a kernel is refused).
  * Errors: INVALID_ARG, UNSUPPORTED_SHAPE, MISALIGNED, DEVICE_STATUS (GNF4_CHECK), CUDA.
  */
 gnf4_status gnf4_lora_apply(const void* base, const void* x, int dtype, const void* A, const void* B,

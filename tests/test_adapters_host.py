@@ -114,6 +114,16 @@ def test_act8_refusals():
     assert b"device memory" in lib.gnf4_last_error()
 
 
+def test_stall_is_refused_where_no_kernel_waits():
+    stall = _lib.GNF4_TEST_STALL
+    assert apply(r=72, flags=stall) == INVALID and b"nothing waits" in lib.gnf4_last_error()
+    assert lib.gnf4_lora_grad_a(FAKE, FAKE, None, None, FAKE, None, 4, 32, 256, 8, 8, FAKE, 0, stall, None) == INVALID
+    assert b"nothing waits" in lib.gnf4_last_error()
+    for call in (lambda: apply(flags=stall), lambda: backward(flags=stall),        # let in, but no device memory
+                 lambda: lib.gnf4_lora_grad_a(FAKE, FAKE, None, None, FAKE, None, 4, 40, 256, 8, 8, FAKE, 0, stall, None)):
+        assert call() == INVALID and b"device memory" in lib.gnf4_last_error()
+
+
 def test_sizes_past_one_pass_of_a_grid_are_refused():
     # 2^41 elements are let in (and then refused as no device memory); there is no second pass beyond
     most = 1 << 41

@@ -618,6 +618,37 @@ def test_other_stream():
     assert torch.equal(out, want) and all(torch.equal(a, b) for a, b in zip(got, ref))
 
 
+@pytest.mark.parametrize("r,counts", [(16, [9, 0, 30]), (32, [40] * 100), (64, [2600, 1]), (40, [3]), (128, [50, 0, 700])])
+def test_waits_that_give_up_are_reported_and_the_next_call_is_right(r, counts):
+    """GNF4_TEST_STALL: the streaming kernel issues no copy and the gradient sums of ranks above 32
+    no matrix product, so every first wait gives up after a short limit with nothing in flight.
+    gnf4_device_status reports it once, and rows that do not exist stay as they were."""
+    g = lib()
+    p = Problem(counts, r, 136, 200, seed=r, spare=4)
+    h, gh = torch.randn(p.R + 4, r, device="cuda"), torch.full((p.R + 4, r), 5.0, device="cuda")
+    dy, dx = torch.randn_like(p.base), torch.full((p.R + 4, 136), 3.0, device="cuda").to(torch.bfloat16)
+
+    def given_up(call):
+        call()
+        with pytest.raises(g.Gnf4Error) as e:
+            g.device_status()
+        assert e.value.status == 5 and "adapters" in str(e.value)
+        g.device_status()                                # the record was cleared
+
+    if r <= 64:
+        out = p.base.clone()
+        given_up(lambda: g.lora_apply(p.base, p.x, p.A, p.B, p.offsets, row_dest=p.dest, out=out, flags=g.GNF4_TEST_STALL, **p.rows()))
+        assert torch.equal(out, p.base)                  # the sums were skipped
+    given_up(lambda: g.lora_backward(dy, h, p.A, p.B, p.offsets, x=p.x, row_src=p.dest, dx=dx, grad_h=gh,
+                                     flags=g.GNF4_TEST_STALL, **p.rows()))
+    assert (dx[p.R:] == 3).all() and (gh[p.R:] == 5).all()
+    if r > 32:
+        given_up(lambda: g.lora_grad_a(h, p.offsets, x=p.x, row_token=p.tok, flags=g.GNF4_TEST_STALL))
+    p.check_forward()
+    p.check_backward(torch.float32)
+    g.device_status()
+
+
 def test_requests_through_routing_metadata():
     """Adapter ids of a batch of tokens, some without one, on top of one shared 4-bit projection."""
     g = lib()
