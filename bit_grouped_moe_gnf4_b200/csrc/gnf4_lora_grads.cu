@@ -47,11 +47,15 @@ struct GradShape {
     static constexpr size_t work = kGradStages * stage_bytes + 2 * plane_bytes + 2 * SR * 4;
     static constexpr size_t sums = sizeof(float) * (size_t)kLoraWarps * RP * kStride;
     static constexpr size_t smem = work > sums ? work : sums;
+    static constexpr int kTotals = 64 * MT;              // columns of tensor memory: a warp's accumulators lie on its 32 lanes
+    // with so much shared memory beside them, the CTAs that an SM holds never want more columns than it has
+    static_assert(smem >= kTotals * 456, "tensor memory of an SM");
 };
 
 // One item; more than one part of its rows are those of the CTAs of a cluster.
-template <int RP, int WR, int TERMS, bool Q8>
-__device__ __forceinline__ void grad_body(const LoraGradArgs& p, const LoraGradSide& d, const GradItem& it, uint8_t* smem) {
+template <int RP, int WR, int TERMS, bool Q8, bool MANY>
+__device__ __forceinline__ void grad_body(const LoraGradArgs& p, const LoraGradSide& d, const GradItem& it, uint8_t* smem,
+                                          uint32_t* s_tmem) {
     const int e = it.e, col0 = it.col0, parts = it.parts, part = it.part;
     using S = GradShape<RP, WR, TERMS>;
     constexpr int CT = S::CT, MT = S::MT, WC = S::WC, CW = S::CW, SR = S::SR;
@@ -159,6 +163,34 @@ __device__ __forceinline__ void grad_body(const LoraGradArgs& p, const LoraGradS
 #pragma unroll
             for (int j = 0; j < 4; ++j) acc[m][c][j] = 0.0f;
 
+    // MANY: the accumulators are emptied into totals, which lie in tensor memory, from time to time
+    auto totals = [&]() { return *s_tmem + ((uint32_t)(32 * (warp & 3)) << 16) + (uint32_t)(warp >> 2) * (S::kTotals / 2); };
+    auto add_totals = [&]() {
+        const uint32_t at = totals();
+#pragma unroll
+        for (int m = 0; m < MT; ++m)
+#pragma unroll
+            for (int c = 0; c < CT; ++c) {
+                const float4 v = tmem_load4(at + 32 * m + 4 * c);
+                acc[m][c][0] += v.x;
+                acc[m][c][1] += v.y;
+                acc[m][c][2] += v.z;
+                acc[m][c][3] += v.w;
+            }
+    };
+    auto empty = [&]() {
+        const uint32_t at = totals();
+#pragma unroll
+        for (int m = 0; m < MT; ++m)
+#pragma unroll
+            for (int c = 0; c < CT; ++c) {
+                tmem_store4(at + 32 * m + 4 * c, acc[m][c]);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) acc[m][c][j] = 0.0f;
+            }
+        asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+    };
+
     // prologue: two stages of copies under way, the first stage's left in place
     static_assert(kGradStages == 3, "the prologue and the row buffers are written for three stages");
     if (tid < SR) {
@@ -241,7 +273,12 @@ __device__ __forceinline__ void grad_body(const LoraGradArgs& p, const LoraGradS
                             mma_bf16_16816(acc[m][c], a[m][k][0], a[m][k][1], a[m][k][2], a[m][k][3], code_frag[c][0], code_frag[c][1]);
             }
         }
+        if (MANY && (i + 1) % kGradChain<TERMS> == 0 && i + 1 < stages) {
+            if (i + 1 > kGradChain<TERMS>) add_totals();
+            empty();
+        }
     }
+    if (MANY && stages > kGradChain<TERMS>) add_totals();
     copy_wait<0>();
     __syncthreads();                                     // the stages become the sums' space
 
@@ -311,30 +348,50 @@ __device__ __forceinline__ void grad_body(const LoraGradArgs& p, const LoraGradS
     if (parts > 1) cluster_wait();
 }
 
-template <int RP, int WR, int TERMS, bool Q8>
+template <int RP, int WR, int TERMS, bool Q8, bool MANY>
 __global__ void __launch_bounds__(kLoraThreads, WR == 1 ? 2 : 1) lora_grads_kernel(const LoraGradArgs p) {
     extern __shared__ __align__(16) uint8_t smem[];
     __shared__ GradSearch find;
-    const GradItem it = grad_item(p, GradShape<RP, WR, TERMS>::CW, &find);
+    __shared__ uint32_t s_tmem;
+    using S = GradShape<RP, WR, TERMS>;
+    if constexpr (MANY) {
+        if (threadIdx.x < 32) tmem_alloc<S::kTotals>(&s_tmem);
+        tc_before();
+        __syncthreads();
+        tc_after();
+    }
+    const GradItem it = grad_item(p, S::CW, &find);
     if (it.e < p.L) {
-        if (it.side_b) grad_body<RP, WR, TERMS, false>(p, p.b, it, smem);
-        else grad_body<RP, WR, TERMS, Q8>(p, p.a, it, smem);
+        if (it.side_b) grad_body<RP, WR, TERMS, false, MANY>(p, p.b, it, smem, &s_tmem);
+        else grad_body<RP, WR, TERMS, Q8, MANY>(p, p.a, it, smem, &s_tmem);
+    }
+    if constexpr (MANY) {
+        tc_before();
+        __syncthreads();
+        tc_after();
+        if (threadIdx.x < 32) tmem_free<S::kTotals>(s_tmem);
     }
     // whoever waits for this grid waits for that one too; a CTA without an item leaves its place at once
     if (threadIdx.x == 0 && (it.e < p.L || blockIdx.x == 0)) wait_for_previous_grid();
 }
 
-template <int RP, int WR, int TERMS, bool Q8>
+template <int RP, int WR, int TERMS, bool Q8, bool MANY>
 cudaError_t launch_grads_t(const LoraGradArgs& a, int cs, cudaStream_t s) {
     using S = GradShape<RP, WR, TERMS>;
     static_assert(S::smem <= kMaxSmem, "shared memory of a CTA");
-    return launch_grads_kernel<lora_grads_kernel<RP, WR, TERMS, Q8>>(a, S::CW, cs, (int)S::smem, s);
+    return launch_grads_kernel<lora_grads_kernel<RP, WR, TERMS, Q8, MANY>>(a, S::CW, cs, (int)S::smem, s);
+}
+
+template <int RP, int WR, int TERMS, bool Q8>
+cudaError_t launch_grads_q(const LoraGradArgs& a, int cs, cudaStream_t s) {
+    if (past_chain(a, cs, WR, kGradChain<TERMS>)) return launch_grads_t<RP, WR, TERMS, Q8, true>(a, cs, s);
+    return launch_grads_t<RP, WR, TERMS, Q8, false>(a, cs, s);
 }
 
 template <int RP, int WR>
 cudaError_t launch_grads_w(const LoraGradArgs& a, bool f32, int cs, cudaStream_t s) {
-    if (a.a.codes) return f32 ? launch_grads_t<RP, WR, 3, true>(a, cs, s) : launch_grads_t<RP, WR, 2, true>(a, cs, s);
-    return f32 ? launch_grads_t<RP, WR, 3, false>(a, cs, s) : launch_grads_t<RP, WR, 2, false>(a, cs, s);
+    if (a.a.codes) return f32 ? launch_grads_q<RP, WR, 3, true>(a, cs, s) : launch_grads_q<RP, WR, 2, true>(a, cs, s);
+    return f32 ? launch_grads_q<RP, WR, 3, false>(a, cs, s) : launch_grads_q<RP, WR, 2, false>(a, cs, s);
 }
 
 // How the work is cut. First by columns, all the CTA's warps side by side (WR = 1), with a

@@ -21,6 +21,58 @@ __host__ __device__ __forceinline__ int most_heavy(const LoraGradArgs& p) {
     return n < p.L ? (int)n : p.L;
 }
 
+// An accumulating matrix instruction cuts its sum off at 24 bits instead of rounding it, so a chain of
+// them falls short by up to 2^-23 of the sum each (2^-25.8 on average), always to the same side:
+// 2^20 rows of one adapter, all products positive, left fp32 gradients 1.9e-4 (ranks up to 32) and
+// 7.3e-4 of their value short. So the accumulators are emptied into totals that are added up in fp32,
+// rounded to nearest: with three terms (fp32 results) after 48 instructions, 2^-20 short, with two
+// (bf16 results) after 4096, 2^-13.8, which the result's 2^-9 hides.
+template <int TERMS>
+constexpr int kGradChain = TERMS == 3 ? 8 : 1024;        // stages of 32 rows
+
+__device__ __forceinline__ void tc_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tc_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+// Called by a whole warp, first of all: a CTA of a kernel that allocates tensor memory has its SM to
+// itself until it gives up its permit to.
+template <int COLS>
+__device__ __forceinline__ void tmem_alloc(uint32_t* to) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(to)), "n"(COLS) : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+}
+template <int COLS>
+__device__ __forceinline__ void tmem_free(uint32_t at) {
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(at), "n"(COLS));
+}
+// 16 columns of this warp's lanes
+__device__ __forceinline__ void tmem_load16(float (&v)[16], uint32_t at) {
+    uint32_t u[16];
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+        : "=r"(u[0]), "=r"(u[1]), "=r"(u[2]), "=r"(u[3]), "=r"(u[4]), "=r"(u[5]), "=r"(u[6]), "=r"(u[7]),
+          "=r"(u[8]), "=r"(u[9]), "=r"(u[10]), "=r"(u[11]), "=r"(u[12]), "=r"(u[13]), "=r"(u[14]), "=r"(u[15])
+        : "r"(at));
+    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+    for (int k = 0; k < 16; ++k) v[k] = __uint_as_float(u[k]);
+}
+__device__ __forceinline__ void tmem_store16(uint32_t at, const float (&v)[16]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};"
+        ::"r"(at), "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7]),
+          "f"(v[8]), "f"(v[9]), "f"(v[10]), "f"(v[11]), "f"(v[12]), "f"(v[13]), "f"(v[14]), "f"(v[15]) : "memory");
+}
+// 4 columns
+__device__ __forceinline__ float4 tmem_load4(uint32_t at) {
+    float4 v;
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x4.b32 {%0,%1,%2,%3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(at));
+    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+    return v;
+}
+__device__ __forceinline__ void tmem_store4(uint32_t at, const float (&v)[4]) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%0], {%1,%2,%3,%4};"
+                 ::"r"(at), "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]) : "memory");
+}
+
 struct GradItem {
     int e;                      // the adapter; L: nothing to do
     int col0, parts, part;      // first column; of how many parts of the rows this CTA has which
@@ -137,6 +189,17 @@ inline int heavy_rows(int64_t R, int64_t avg) {
     int64_t heavy = 4 * avg > 256 ? 4 * avg : 256;
     if (heavy < R / 32) heavy = R / 32;
     return avg < 8 || R < 1024 || heavy >= R ? 0 : (int)heavy;
+}
+
+// Whether a CTA (or `warps` of its warps that share the rows of a stage) can get more rows than a chain
+// has: all rows may be one adapter's, which the cs CTAs of its cluster share, or a single CTA
+// has the rows from which an adapter is heavy. The kernels with totals take longer, us of a backward
+// pass with fp32 results at 2048 and 1536 columns, without and with them: 128 adapters, 32768 rows,
+// rank 16 131.7 and 136.2, rank 32 174.0 and 179.9; 64 adapters, 8192 rows, rank 64 87.5 and 92.7,
+// rank 128 219 and 222; one adapter of 65536 rows, rank 32 414 and 429, rank 64 575 and 624.
+inline bool past_chain(const LoraGradArgs& a, int cs, int warps, int chain) {
+    const int64_t most = a.heavy * (int64_t)cs > a.R ? a.heavy * (int64_t)cs : a.R;
+    return most > (int64_t)32 * chain * warps * cs;
 }
 
 // ranks above 32 (gnf4_lora_grads_wide.cu)

@@ -5,8 +5,8 @@
 // 32. D [terms x rank, CW] += left^T right, rows the contraction index: both operands lie in
 // shared memory as they come, row by row, contiguous across the contraction, and one thread has
 // tcgen05.mma read them there. The terms of `left` are rows of one MMA side by side (128 in all,
-// three terms of rank 64 take two and of rank 128 three) and are added up at the end, when the
-// accumulator leaves tensor memory. The rows of `right` are copied straight to their swizzled
+// three terms of rank 64 take two and of rank 128 three) and are added up when the accumulator
+// leaves tensor memory, at the end and, with very many rows (kGradChain), from time to time. The rows of `right` are copied straight to their swizzled
 // place by 16-byte asynchronous copies, two stages ahead; codes and `left` go through the threads
 // that copied them, which make bf16 of the one and the terms of the other.
 //
@@ -32,7 +32,7 @@ namespace {
 
 constexpr int kGradRows = 32;                            // rows of a stage
 
-template <int RP, int TERMS, bool Q8>
+template <int RP, int TERMS, bool Q8, bool MANY>
 struct GradShape {
     static constexpr int CW = RP == 64 ? 256 : 128;       // columns of a CTA, two of which share an SM
     static constexpr int S = 3;                          // stages
@@ -51,7 +51,8 @@ struct GradShape {
     // so much at least that no more CTAs share an SM than its 512 columns of tensor memory serve:
     // one that waited for columns would hold up its cluster, and clusters could so wait for
     // one another
-    static constexpr int least = CW * 456 - 1024;
+    static constexpr int kCols = MANY && SLOTS == 1 ? 2 * CW : CW;      // of tensor memory: the accumulator, and totals behind it
+    static constexpr int least = kCols * 456 - 1024;
     static constexpr int need = 128 + 1023 + (work > sums ? work : sums);       // behind GradControl, at a multiple of 1024
     static constexpr int smem = need > least ? need : least;
 };
@@ -76,18 +77,16 @@ __device__ __forceinline__ uint64_t desc_across(uint32_t saddr, uint32_t next) {
 __device__ __forceinline__ uint32_t across(int m, int k, int rows) {
     return (uint32_t)((m >> 6) * (rows * 128) + k * 128 + ((((m & 63) >> 3) ^ (k & 7)) << 4) + (m & 7) * 2);
 }
-__device__ __forceinline__ void tc_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
-__device__ __forceinline__ void tc_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void copy_async4(uint32_t dst, const void* src) {
     asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
 }
 
 // One item; more than one part of its rows are those of the CTAs of a cluster.
-template <int RP, int TERMS, bool Q8>
+template <int RP, int TERMS, bool Q8, bool MANY>
 __device__ __forceinline__ void grad_body(const LoraGradArgs& p, const LoraGradSide& d, const GradItem& it, uint8_t* smem,
                                           GradControl* ctl) {
     const int e = it.e, col0 = it.col0, parts = it.parts, part = it.part;
-    using S = GradShape<RP, TERMS, Q8>;
+    using S = GradShape<RP, TERMS, Q8, MANY>;
     constexpr int CW = S::CW, SR = kGradRows, D = S::S - 1;     // stages that the copies are ahead
     constexpr int LPR = S::raw / SR / 16, RPI = 32 / LPR;    // lanes that copy a row, rows a warp copies at a time
     constexpr int BPR = CW / 32;                             // a row's blocks of a checkpoint
@@ -150,7 +149,8 @@ __device__ __forceinline__ void grad_body(const LoraGradArgs& p, const LoraGradS
             }
         }
     };
-    // the stage's left, split into terms: matrix row SLOT * RP + j of MMA q holds term q * SLOTS + SLOT
+    // the stage's left, split into terms: of 16 SLOTS matrix rows of MMA q the first 16 hold term
+    // q * SLOTS of 16 ranks, the next 16 (where there are two SLOTS) the next term of the same ranks
     auto make_left = [&](int i) {
         const uint32_t from = stage0 + (uint32_t)(i % S::S * S::stage + S::raw);
         const uint32_t to = made0;
@@ -166,7 +166,7 @@ __device__ __forceinline__ void grad_body(const LoraGradArgs& p, const LoraGradS
             split_pair<TERMS, false>(__uint_as_float(v.z) * f, __uint_as_float(v.w) * f, b);
 #pragma unroll
             for (int t = 0; t < TERMS; ++t) {
-                const uint32_t at = to + (uint32_t)(t / S::SLOTS * S::MM * SR * 2) + across(t % S::SLOTS * RP + j, k, SR);
+                const uint32_t at = to + (uint32_t)(t / S::SLOTS * S::MM * SR * 2) + across(16 * S::SLOTS * (j / 16) + 16 * (t % S::SLOTS) + j % 16, k, SR);
                 asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(at), "r"(a[t]), "r"(b[t]) : "memory");
             }
         }
@@ -211,13 +211,62 @@ __device__ __forceinline__ void grad_body(const LoraGradArgs& p, const LoraGradS
         if (i < stages) copy_left(i);
         copy_commit();
     }
-    if constexpr (TERMS % S::SLOTS != 0 && S::MMAS > 1) {    // the rows of the last MMA that no term fills
-        for (int i = tid; i < (S::MMAS * S::SLOTS - TERMS) * RP * SR * 2 / 16; i += kLoraThreads)
-            *reinterpret_cast<uint4*>(smem + S::S * S::stage + TERMS * RP * SR * 2 + i * 16) = make_uint4(0, 0, 0, 0);
+    if constexpr (TERMS % S::SLOTS != 0) {               // the rows of the last MMA that no term fills
+        static_assert(S::SLOTS <= 2 && S::MM * SR * 2 / 16 == 2 * kLoraThreads, "half of the matrix's 16-byte pieces");
+        const int k = tid & 31, m = 32 * (tid >> 6) + 16 + 8 * (tid >> 5 & 1);
+        asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};"
+                     ::"r"(made0 + (uint32_t)((S::MMAS - 1) * S::MM * SR * 2) + across(m, k, SR)), "r"(0u) : "memory");
     }
 
     const uint32_t tmem = ctl->tmem;
     bool gone = false;
+    // MANY: totals that the accumulator is emptied into. 64 columns a thread of one rank, half of the accumulator's for the 32 lanes (matrix
+    // rows) that a warp reads. With two SLOTS lanes 16 to 31 hold the other term of the ranks of lanes 0
+    // to 15, each of a pair of lanes keeps one half of its columns, and the totals lie in
+    // registers: the accumulators of two CTAs fill the SM's tensor memory. Else they lie behind the accumulator.
+    constexpr int CHAIN = kGradChain<TERMS>;
+    const int quarter = warp & 3, half = warp >> 2;
+    const bool upper = S::SLOTS == 2 && lane >= 16;
+    const uint32_t sums = tmem + ((uint32_t)(32 * quarter) << 16) + (uint32_t)(half * (CW / 2));
+    constexpr bool REGS = MANY && S::SLOTS == 2;
+    float total[REGS ? 64 : 1];
+#pragma unroll
+    for (int c = 0; c < (REGS ? 64 : 1); ++c) total[c] = 0.0f;
+    // 16 of this thread's columns of the accumulator, terms added up, from column c on
+    auto read = [&](int c, float (&v)[16]) {
+        tmem_load16(v, sums + c);
+        if constexpr (S::SLOTS == 2) {
+            float w[16];
+            tmem_load16(w, sums + 64 + c);
+#pragma unroll
+            for (int k = 0; k < 16; ++k) {
+                const float other = __shfl_xor_sync(0xffffffffu, upper ? v[k] : w[k], 16);
+                v[k] = (upper ? w[k] : v[k]) + other;
+            }
+        }
+    };
+    auto empty = [&](bool first) {
+        tc_after();
+#pragma unroll
+        for (int c = 0; c < 64; c += 16) {
+            float v[16];
+            read(c, v);
+            if constexpr (REGS) {
+#pragma unroll
+                for (int k = 0; k < 16; ++k) total[c + k] += v[k];
+            } else {
+                if (!first) {
+                    float u[16];
+                    tmem_load16(u, sums + CW + c);
+#pragma unroll
+                    for (int k = 0; k < 16; ++k) v[k] += u[k];
+                }
+                tmem_store16(sums + CW + c, v);
+            }
+        }
+        if constexpr (!REGS) asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+        tc_before();
+    };
     auto wait_made = [&](int i) {                        // the MMAs of stage i are through
         if (!gone)
             gone = !mbar_wait_bounded(smem_addr(&ctl->done), (uint32_t)(i & 1), &ctl->abort, &g_grads_err, 1u,
@@ -235,6 +284,9 @@ __device__ __forceinline__ void grad_body(const LoraGradArgs& p, const LoraGradS
             copy_left(i + D);
         }
         copy_commit();
+        if constexpr (MANY) {
+            if (i > 0 && i % CHAIN == 0) empty(i == CHAIN);              // the next product starts from nothing
+        }
         make_left(i);
         if constexpr (Q8) {
             if (i && (i & 7) == 0) {
@@ -260,7 +312,7 @@ __device__ __forceinline__ void grad_body(const LoraGradArgs& p, const LoraGradS
                         "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
                         " tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n"
                         ::"r"(tmem), "l"(desc_across(a + (uint32_t)(m * S::MM * SR * 2 + k * 2048), SR * 128)),
-                          "l"(desc_across(b + (uint32_t)(k * 2048), SR * 128)), "r"(idesc), "r"((uint32_t)(i | k | m)) : "memory");
+                          "l"(desc_across(b + (uint32_t)(k * 2048), SR * 128)), "r"(idesc), "r"((uint32_t)((MANY ? i % CHAIN : i) | k | m)) : "memory");
             asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];"
                          ::"r"(smem_addr(&ctl->done)) : "memory");
         }
@@ -270,39 +322,33 @@ __device__ __forceinline__ void grad_body(const LoraGradArgs& p, const LoraGradS
     tc_after();
     __syncthreads();                                     // the stages become the sums' space
 
-    // the accumulator, a matrix row a lane; its terms are added up one after the other
     float* s_red = reinterpret_cast<float*>(smem);
-    const int quarter = warp & 3, half = warp >> 2;      // lanes and columns that this warp reads
-    const int m = 32 * quarter + lane, slot = 32 * quarter / RP;
+    static_assert(CW / 2 == 64 * S::SLOTS, "columns of a thread's totals");
+    {
+        const int j = S::SLOTS == 2 ? 16 * quarter + (lane & 15) : 32 * quarter + lane;
+        float4* to = reinterpret_cast<float4*>(s_red + j * S::kStride + half * (CW / 2) + (upper ? 64 : 0));
 #pragma unroll
-    for (int t = 0; t < (TERMS < S::SLOTS ? TERMS : S::SLOTS); ++t) {
-        if (slot == t) {
+        for (int c = 0; c < 64; c += 16) {
+            float v[16];
 #pragma unroll
-            for (int c0 = 0; c0 < CW / 2; c0 += 16) {
-                const int c = half * (CW / 2) + c0;
-                uint32_t v[16];
-                asm volatile(
-                    "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
-                    : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]),
-                      "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15])
-                    : "r"(tmem + ((uint32_t)(32 * quarter) << 16) + (uint32_t)c));
-                asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
-                float4* to = reinterpret_cast<float4*>(s_red + (m - slot * RP) * S::kStride + c);
+            for (int k = 0; k < 16; ++k) v[k] = 0.0f;
+            if (stages > 0) {                            // else nothing was ever written there
+                read(c, v);
+                if constexpr (REGS) {
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    float4 f = t ? to[k] : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-                    if (stages > 0) {                // else nothing was ever written there
-                        f.x += __uint_as_float(v[4 * k]);
-                        f.y += __uint_as_float(v[4 * k + 1]);
-                        f.z += __uint_as_float(v[4 * k + 2]);
-                        f.w += __uint_as_float(v[4 * k + 3]);
-                    }
-                    to[k] = f;
+                    for (int k = 0; k < 16; ++k) v[k] += total[c + k];
+                } else if (MANY && stages > CHAIN) {
+                    float u[16];
+                    tmem_load16(u, sums + CW + c);
+#pragma unroll
+                    for (int k = 0; k < 16; ++k) v[k] += u[k];
                 }
             }
+#pragma unroll
+            for (int k = 0; k < 4; ++k) to[c / 4 + k] = make_float4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
         }
-        __syncthreads();
     }
+    __syncthreads();
     // the cluster's CTAs share the columns out and add up theirs, in place: no other CTA reads those
     const int own = CW / parts, own0 = part * own;
     if (parts > 1) {
@@ -340,16 +386,14 @@ __device__ __forceinline__ void grad_body(const LoraGradArgs& p, const LoraGradS
     if (parts > 1) cluster_wait();
 }
 
-template <int RP, int TERMS, bool Q8>
+template <int RP, int TERMS, bool Q8, bool MANY>
 __global__ void __launch_bounds__(kLoraThreads, 2) lora_grads_wide_kernel(const LoraGradArgs p) {
     extern __shared__ __align__(1024) uint8_t smem[];
     uint8_t* buffers = smem + ((0u - smem_addr(smem) - (uint32_t)sizeof(GradControl) & 1023u) + sizeof(GradControl));
-    constexpr int CW = GradShape<RP, TERMS, Q8>::CW;
+    using S = GradShape<RP, TERMS, Q8, MANY>;
+    constexpr int CW = S::CW;
     GradControl* ctl = reinterpret_cast<GradControl*>(smem);
-    if (threadIdx.x < 32) {
-        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(&ctl->tmem)), "n"(CW) : "memory");
-        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
-    }
+    if (threadIdx.x < 32) tmem_alloc<S::kCols>(&ctl->tmem);
     if (threadIdx.x == 0) {
         mbar_init(smem_addr(&ctl->done), 1);
         ctl->abort = 0;
@@ -360,29 +404,36 @@ __global__ void __launch_bounds__(kLoraThreads, 2) lora_grads_wide_kernel(const 
     tc_after();
     const GradItem it = grad_item(p, CW, &ctl->find);
     if (it.e < p.L) {
-        if (it.side_b) grad_body<RP, TERMS, false>(p, p.b, it, buffers, ctl);
-        else grad_body<RP, TERMS, Q8>(p, p.a, it, buffers, ctl);
+        if (it.side_b) grad_body<RP, TERMS, false, MANY>(p, p.b, it, buffers, ctl);
+        else grad_body<RP, TERMS, Q8, MANY>(p, p.a, it, buffers, ctl);
     }
     tc_before();
     __syncthreads();
     tc_after();
-    if (threadIdx.x < 32) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(ctl->tmem), "n"(CW));
+    if (threadIdx.x < 32) tmem_free<S::kCols>(ctl->tmem);
     // whoever waits for this grid waits for that one too; a CTA without an item leaves its place at once
     if (threadIdx.x == 0 && (it.e < p.L || blockIdx.x == 0)) wait_for_previous_grid();
 }
 
-template <int RP, int TERMS, bool Q8>
+template <int RP, int TERMS, bool Q8, bool MANY>
 cudaError_t launch_wide_t(const LoraGradArgs& a, int cs, cudaStream_t s) {
-    constexpr int own = GradShape<RP, TERMS, Q8>::smem, other = GradShape<RP, TERMS, false>::smem;
+    using S = GradShape<RP, TERMS, Q8, MANY>;
+    constexpr int own = S::smem, other = GradShape<RP, TERMS, false, MANY>::smem;
     constexpr int smem = own > other ? own : other;
     static_assert(2 * (smem + 1024) <= 228 * 1024, "shared memory of an SM");
-    return launch_grads_kernel<lora_grads_wide_kernel<RP, TERMS, Q8>>(a, GradShape<RP, TERMS, Q8>::CW, cs, smem, s);
+    return launch_grads_kernel<lora_grads_wide_kernel<RP, TERMS, Q8, MANY>>(a, S::CW, cs, smem, s);
+}
+
+template <int RP, int TERMS, bool Q8>
+cudaError_t launch_wide_q(const LoraGradArgs& a, int cs, cudaStream_t s) {
+    if (past_chain(a, cs, 1, kGradChain<TERMS>)) return launch_wide_t<RP, TERMS, Q8, true>(a, cs, s);
+    return launch_wide_t<RP, TERMS, Q8, false>(a, cs, s);
 }
 
 template <int RP>
 cudaError_t launch_wide_w(const LoraGradArgs& a, bool f32, int cs, cudaStream_t s) {
-    if (a.a.codes) return f32 ? launch_wide_t<RP, 3, true>(a, cs, s) : launch_wide_t<RP, 2, true>(a, cs, s);
-    return f32 ? launch_wide_t<RP, 3, false>(a, cs, s) : launch_wide_t<RP, 2, false>(a, cs, s);
+    if (a.a.codes) return f32 ? launch_wide_q<RP, 3, true>(a, cs, s) : launch_wide_q<RP, 2, true>(a, cs, s);
+    return f32 ? launch_wide_q<RP, 3, false>(a, cs, s) : launch_wide_q<RP, 2, false>(a, cs, s);
 }
 
 // A cluster along an adapter's rows as long as they fit on the SMs at once and keep 128 rows each
@@ -391,7 +442,7 @@ cudaError_t launch_wide_w(const LoraGradArgs& a, bool f32, int cs, cudaStream_t 
 // first case above, 98 and not 90 with shares like 1 / e.
 template <int RP>
 cudaError_t launch_wide_r(const LoraGradArgs& a, bool f32, cudaStream_t s) {
-    constexpr int CW = GradShape<RP, 2, false>::CW;
+    constexpr int CW = GradShape<RP, 2, false, false>::CW;
     const int64_t active = a.R < a.L ? (a.R > 0 ? a.R : 1) : a.L;
     const int64_t avg = (a.R + active - 1) / active, room = 2 * (int64_t)device_sm_count();
     const int64_t items = active * (grad_items(a.a, CW) + grad_items(a.b, CW));

@@ -313,6 +313,50 @@ def test_one_adapter_of_many_does_not_wait_for_its_rows_one_after_the_other():
     assert took[1] < 2.4 * took[0], took
 
 
+@pytest.mark.parametrize("r", [16, 24, 64, 128])
+@pytest.mark.parametrize("counts", [[1 << 20], [0, 1 << 18] + [4] * 198])
+def test_long_sums_lose_nothing(counts, r):
+    """fp32 gradients of an adapter of very many rows, all products positive or of either sign. At most
+    48 matrix instructions follow one another (eight stages, two steps of 16 rows, three terms),
+    each off by 2^-23 of its own short sum; those sums are added up, rounded to nearest (2^-24 of
+    the total each), 256 rows at a time along the eighth (here a quarter with 200 adapters) of the
+    rows that a CTA has. 16 for the three terms' remainders and the joins. In one unbroken chain of
+    truncated sums the error was 2^-26 of the total for every instruction. A bf16 result's chains
+    have 4096 instructions; of its own it has the rounding and 2^-17 for the terms."""
+    g = lib()
+    m, parts = max(counts), 8 if len(counts) == 1 else 4
+    R, K, N = sum(counts), 32, 24
+    gen = torch.Generator(device="cuda").manual_seed(r)
+    off = torch.from_numpy(np.concatenate([[0], np.cumsum(counts)])).cuda()
+    e = int(np.argmax(counts))
+    lo = int(off[e])
+    A, B = torch.zeros(len(counts), r, K, device="cuda").bfloat16(), torch.zeros(len(counts), N, r, device="cuda").bfloat16()
+    tol = (48 + 16) * 2.0 ** -23 + m / parts / 256 * 2.0 ** -24
+    for positive in (True, False):
+        rand = (lambda *s: torch.rand(*s, generator=gen, device="cuda")) if positive else \
+               (lambda *s: torch.randn(*s, generator=gen, device="cuda"))  # noqa: E731
+        x, dy, h = rand(R, K).to(torch.bfloat16), rand(R, N).to(torch.bfloat16), rand(R, r)
+        dA = g.lora_grad_a(h, off, x=x, grad_dtype=torch.float32)
+        q = g.quantize_act8(x)
+        dA8 = g.lora_grad_a(h, off, act8=q, grad_dtype=torch.float32)
+        dB = g.lora_backward(dy, h, A, B, off, x=x, want_dx=False, grad_dtype=torch.float32)[2]
+        half = g.lora_grad_a(h, off, x=x)
+        for got, left, right, what in ((dA, h, x, "dA"), (dA8, h, g.dequantize_act8(*q), "dA from codes"), (dB, dy, h, "dB"),
+                                       (half, h, x, "bf16 dA")):
+            want = torch.zeros(got[e].shape, dtype=torch.float64, device="cuda")
+            bound = want.clone()
+            for a, b in zip(left[lo:lo + m].split(1 << 17), right[lo:lo + m].split(1 << 17)):
+                want += a.double().T @ b.double()
+                bound += a.double().abs().T @ b.double().abs()
+            err = (got[e].double() - want).abs()
+            if got is half:
+                allowed = tol + (4096 - 48) * 2.0 ** -23 + 2.0 ** -16
+                assert (err <= 2.0 ** -8 * want.abs() + (1 + 2.0 ** -8) * allowed * bound).all(), what
+            else:
+                worst = float((err / bound).max())
+                assert worst <= tol, f"{what}, positive {positive}: {worst:.3g} of the magnitudes, {tol:.3g} allowed"
+
+
 def test_in_place_and_deterministic():
     p = Problem([7, 0, 50, 1], 16, 256, 320)
     out, _ = p.forward()
