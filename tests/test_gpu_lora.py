@@ -313,6 +313,41 @@ def test_one_adapter_of_many_does_not_wait_for_its_rows_one_after_the_other():
     assert took[1] < 2.4 * took[0], took
 
 
+def bf16_terms(v, n):
+    """The sum of n bf16 numbers, each the rounding of what the ones before it leave (fp64 arrays)."""
+    total = np.zeros_like(v)
+    for _ in range(n):
+        total += O.bf16_to_f64(O.bf16_bits(v - total))
+    return total
+
+
+@pytest.mark.parametrize("r", [8, 32, 40, 128])
+@pytest.mark.parametrize("act8", [False, True])
+def test_fp32_gradients_of_single_rows_have_all_bits(r, act8):
+    """One row an adapter: a gradient is one product of a 24-bit and an 8-bit number. Three bf16 terms
+    leave 2^-27 of the first; the three products are exact and added up with 2^-23 each, and the
+    result is fp32. With the first two terms alone the oracle's own products are past the tolerance."""
+    g = lib()
+    L, K, N = 5, 96, 72
+    gen = torch.Generator(device="cuda").manual_seed(r)
+    rand = lambda *s: torch.randn(*s, generator=gen, device="cuda")  # noqa: E731
+    x, dy, h = rand(L, K).to(torch.bfloat16), rand(L, N).to(torch.bfloat16), rand(L, r)
+    A, B = rand(L, r, K).to(torch.bfloat16), rand(L, N, r).to(torch.bfloat16)
+    off = torch.arange(L + 1, device="cuda")
+    gh = torch.empty(L, r, device="cuda")
+    q = g.quantize_act8(x)
+    src, xv = (dict(act8=q), A8.values_act8(q[0].cpu().numpy(), q[1].cpu().numpy())) if act8 else (dict(x=x), f64(x))
+    _, dA, dB = g.lora_backward(dy, h, A, B, off, grad_h=gh, grad_dtype=torch.float32, **src)
+    tol = 2.0 ** -27 + 3 * 2.0 ** -23 + 2.0 ** -24
+    for got, left, outer in ((dA, f64(gh), lambda v: v[:, :, None] * xv[:, None, :]),
+                             (dB, f64(h), lambda v: f64(dy)[:, :, None] * v[:, None, :])):
+        want = outer(left)
+        err = np.abs(f64(got) - want)
+        assert np.all(err <= tol * np.abs(want)), float((err / np.abs(want).clip(1e-300)).max())
+        assert np.any(np.abs(outer(bf16_terms(left, 2)) - want) > 2 * tol * np.abs(want))
+        assert np.all(np.abs(outer(bf16_terms(left, 3)) - want) <= 2.0 ** -26 * np.abs(want))
+
+
 @pytest.mark.parametrize("r", [16, 24, 64, 128])
 @pytest.mark.parametrize("counts", [[1 << 20], [0, 1 << 18] + [4] * 198])
 def test_long_sums_lose_nothing(counts, r):
@@ -374,6 +409,34 @@ def test_in_place_and_deterministic():
     want = g.lora_backward(dy, h, p.A, p.B, p.offsets, dx_base=dxb, **kw)[0]
     got = g.lora_backward(dy, h, p.A, p.B, p.offsets, dx_base=dxb, dx=dxb, **kw)[0]
     assert got is dxb and torch.equal(got, want)
+
+
+@pytest.mark.parametrize("r", [16, 32, 64, 128])
+@pytest.mark.parametrize("counts", [[3, 0, 1], [40] * 30, [900, 0, 1600, 33], [2100] + [9] * 100])
+@pytest.mark.parametrize("grads", [torch.bfloat16, torch.float32])
+def test_a_call_repeats_itself_behind_others(counts, r, grads):
+    # the same inputs, at first alone, then with other calls before and after and nothing waited for
+    g = lib()
+    one, two = (Problem(counts, r, 264, 200, seed=s) for s in (1, 2))
+    for p in (one, two):
+        p.dy, p.hh = torch.randn_like(p.base), torch.randn(p.R, r, device="cuda")
+
+    def step(p):
+        h = torch.empty(p.R, r, device="cuda")
+        out = g.lora_apply(p.base, p.x, p.A, p.B, p.offsets, row_dest=p.dest, out=p.base.clone(), h=h, **p.rows())
+        return (out, h, *g.lora_backward(p.dy, p.hh, p.A, p.B, p.offsets, x=p.x, row_src=p.dest, grad_dtype=grads, **p.rows()))
+
+    torch.cuda.synchronize()
+    want = step(one)
+    torch.cuda.synchronize()
+    got = []
+    for _ in range(4):
+        step(two)
+        got.append(step(one))
+        step(two)
+    torch.cuda.synchronize()
+    for again in got:
+        assert all(torch.equal(a, b) for a, b in zip(again, want))
 
 
 def test_base_none_is_zeros():
