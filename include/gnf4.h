@@ -440,7 +440,11 @@ gnf4_status gnf4_swiglu_backward(const void* grad_out, const void* gate_up, cons
  * Sums in fp32 by matrix instructions, which cut off what is below 24 bits: h (and grad_h) falls
  * short by about K 2^-33 (N 2^-33) of the sum of its products' magnitudes, 2^-20 at 8192. h enters
  * the second product with about 17 significant bits (two 16-bit terms).
- * Deterministic: the same call gives the same bits. R == 0 launches nothing and accepts NULL
+ * Deterministic: the same call gives the same bits. A row's bits (out and h, the backward's dx and
+ * grad_h) do not depend on the other rows as long as R and L are the same, whatever the offsets
+ * say: a captured call gives a token the same bits in every batch. Calls of another R or L may
+ * choose another split of the sums over K, so unlike the decode band's the bits are not those of any
+ * row count. R == 0 launches nothing and accepts NULL
  * buffers; with R > 0, T_in (the backward's T_g) is at least 1.
  * flags: GNF4_CHECK (validates offsets, row arrays and weights on the device first: one extra kernel
  * and a stream sync) and GNF4_TEST_STALL (testing the error path as in the grouped call: the kernels
@@ -468,7 +472,8 @@ gnf4_status gnf4_lora_apply(const void* base, const void* x, int dtype, const vo
  * x          device bf16 [T_in, K], or NULL: then x_codes int8 [T_in, K] (16-byte aligned) and
  *            x_scales uint8 [T_in, K/32] hold its checkpoint (K % 32 == 0)
  * h          device fp32 [R, r] as the forward wrote it
- * dx         device bf16 [R, K], may be dx_base; or NULL (with dx_base NULL): not wanted
+ * dx         device bf16 [R, K], may be dx_base; or NULL (with dx_base NULL): not wanted (its writes
+ *            are saved, the product behind it is computed all the same)
  * grad_h     device fp32 [R, r] (written)
  * dA, dB     device [L, r, K] and [L, N, r] of grad_dtype: GNF4_DTYPE_BF16 or GNF4_DTYPE_F32
  *            (fp32 sums, rounded once; over any number of rows fp32 results fall short by no

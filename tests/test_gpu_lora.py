@@ -439,6 +439,32 @@ def test_a_call_repeats_itself_behind_others(counts, r, grads):
         assert all(torch.equal(a, b) for a, b in zip(again, want))
 
 
+@pytest.mark.parametrize("r", [16, 24, 64, 128])
+@pytest.mark.parametrize("R", [40, 300, 2600, 21000])
+def test_a_rows_bits_do_not_depend_on_the_others(r, R):
+    # one token of adapter 3, alone and among others, in the same R and L: every split that the calls choose
+    g = lib()
+    L, K, N = 5, 392, 328
+    gen = torch.Generator(device="cuda").manual_seed(R)
+    rand = lambda *s: torch.randn(*s, generator=gen, device="cuda").to(torch.bfloat16)  # noqa: E731
+    A, B, scal = rand(L, r, K), rand(L, N, r), torch.rand(L, generator=gen, device="cuda")
+    token, above, behind, under = rand(1, K), rand(1, N), rand(1, N), rand(1, K)
+    seen = []
+    for before, after in (([0, 0, 0], [0, 0]), ([7, 0, 3], [9, 0]), ([0, R // 3, 1], [R // 4, 5])):
+        at = sum(before)
+        counts = before + [1 + after[0], after[1]]
+        off = torch.from_numpy(np.concatenate([[0], np.cumsum(counts)])).cuda()
+        x, base, dy, dxb = rand(R, K), rand(R, N), rand(R, N), rand(R, K)
+        for t, row in ((x, token), (base, above), (dy, behind), (dxb, under)):
+            t[at] = row
+        h, gh = torch.zeros(R, r, device="cuda"), torch.zeros(R, r, device="cuda")
+        out = g.lora_apply(base, x, A, B, off, scaling=scal, h=h, R=R)
+        dx, _, _ = g.lora_backward(dy, h, A, B, off, x=x, scaling=scal, dx_base=dxb, grad_h=gh, R=R)
+        seen.append([t[at].clone() for t in (out, h, dx, gh)])
+    for again in seen[1:]:
+        assert all(torch.equal(a, b) for a, b in zip(again, seen[0]))
+
+
 def test_base_none_is_zeros():
     g = lib()
     p = Problem([5, 40], 16, 128, 64, scatter=False)
