@@ -8,9 +8,10 @@
 // once for all warps. Both fragments come out of shared memory transposed.
 //
 // What bounds it is instruction issue: about 330 instructions a warp and stage of 32 rows (the
-// copies' addresses, the split of left, the products; 450 with codes), issue slots 47 % busy
-// and a third of the stalls on loads, with DRAM at a fifth of its rate. 128 experts over 32768
-// rows, rank 16, 2048 checkpointed and 1536 columns: 64 us. Warps that only copy beside warps
+// copies' addresses, the split of left, the products; 450 with codes). 128 experts over 32768 rows,
+// rank 16, 2048 checkpointed and 1536 columns: issue slots 46 % busy, the stalls led by fixed
+// latency (1.9 cycles an instruction) and barriers (1.2), loads and shared memory 0.8 each, DRAM
+// at 18 % of its rate, the tensor pipe at 18 %; 64 us. Warps that only copy beside warps
 // that only multiply took 65 to 75 us there, with bulk copies of a row (52 to 67 cycles each
 // from one CTA) or 16-byte ones.
 #include <cstdint>

@@ -447,7 +447,9 @@ cudaError_t launch_lora_rows(const LoraRowsArgs& a, bool bwd, bool f16, cudaStre
     // rank 16, 2048 rows of 64 adapters 12.8 and 14.8 / 13.7 and 14.5, 2400 rows 14.8 and 13.5 /
     // 17.0 and 14.9, 32768 rows of 128 adapters 96.9 and 68.6 / 110.7 and 74.0; rank 64, 2048 rows
     // 18.0 and 22.0 / 25.0 and 23.8, 2400 rows 22.8 and 21.7 / 34.1 and 23.1, 32768 rows 151.7 and
-    // 119.1 / 217.5 and 123.2. (A rank of 128 has no room for the stream's stages.)
+    // 119.1 / 217.5 and 123.2. Ranks above 64 have no streaming kernel: its stages of 256 columns do not
+    // fit beside them (stages of 128 would), so their rows' factors are read once per 16 rows:
+    // 8192 rows of 64 adapters, rank 64 36.7 us, rank 72 91.8, rank 128 100.
     if (a.r <= 64 && (a.test_stall || a.R >= 16 * (int64_t)device_sm_count())) return launch_lora_stream(a, bwd, f16, s);
     if (a.r <= 16) return launch_rows<16>(a, bwd, f16, s);
     if (a.r <= 32) return launch_rows<32>(a, bwd, f16, s);
