@@ -62,6 +62,34 @@ def test_checkpoint_of_more_rows_than_one_pass():
     assert np.array_equal(codes[-5:].cpu().numpy(), want_c) and np.array_equal(scales[-5:].cpu().numpy(), want_s)
 
 
+def test_elements_past_32_bits():
+    # more than 2^32 elements in one call; the last rows, the middle and the first against calls of their own
+    g = lib()
+    R, I = (1 << 21) + 37, 1024
+    h = torch.empty(R, 2 * I, dtype=torch.bfloat16, device="cuda").normal_()
+    parts = [slice(0, 40), slice(R // 2 - 20, R // 2 + 20), slice(R - 41, R)]
+    codes, scales = g.quantize_act8(h)
+    back = g.dequantize_act8(codes, scales)
+    for p in parts:
+        want = g.quantize_act8(h[p].clone())
+        assert torch.equal(codes[p], want[0]) and torch.equal(scales[p], want[1])
+        assert torch.equal(back[p], g.dequantize_act8(*want))
+    del back
+    out, c2, s2 = g.swiglu_act8(h)
+    assert torch.equal(c2, codes) and torch.equal(s2, scales)
+    del c2, s2
+    d = out * 0.5
+    for p in parts:
+        assert torch.equal(out[p], g.swiglu(h[p].clone()))
+    dh = g.swiglu_backward(d, act8=(codes, scales), act=out)[0]
+    for p in parts:
+        want = g.swiglu_backward(d[p].clone(), act8=(codes[p].clone(), scales[p].clone()), rebuild=True)
+        assert torch.equal(dh[p], want[0]) and torch.equal(out[p], want[1])
+    g.swiglu_backward(d, gate_up=h, out=dh)
+    for p in parts:
+        assert torch.equal(dh[p], g.swiglu_backward(d[p].clone(), gate_up=h[p].clone()))
+
+
 def test_nothing_is_written_behind_the_rows():
     g = lib()
     codes = torch.full((5 * 96 + 64,), 77, dtype=torch.int8, device="cuda")

@@ -349,7 +349,7 @@ def test_fp32_gradients_of_single_rows_have_all_bits(r, act8):
 
 
 @pytest.mark.parametrize("r", [16, 24, 64, 128])
-@pytest.mark.parametrize("counts", [[1 << 20], [0, 1 << 18] + [4] * 198])
+@pytest.mark.parametrize("counts", [[(1 << 20) + 5000], [0, 1 << 18] + [4] * 198])
 def test_long_sums_lose_nothing(counts, r):
     """fp32 gradients of an adapter of very many rows, all products positive or of either sign. At most
     48 matrix instructions follow one another (eight stages, two steps of 16 rows, three terms),
@@ -641,6 +641,119 @@ def test_far_rows_and_adapters():
     dx1, dA1, dB1 = g.lora_backward(dy, h, A[-1:].contiguous(), B[-1:].contiguous(), off1, x=x)
     assert torch.equal(dx, dx1) and torch.equal(dA[-1:], dA1) and torch.equal(dB[-1:], dB1)
     assert not dA[:-1].any() and not dB[:-1].any()
+
+
+def test_far_rows_of_the_backward():
+    # element offsets past 2^31 in x, its codes, grad_out and what follows from them
+    g = lib()
+    T, K, N, r, n = 1_048_600, 2080, 2056, 40, 300
+    gen = torch.Generator(device="cuda").manual_seed(1)
+    rand = lambda *s: torch.randn(*s, generator=gen, device="cuda").to(torch.bfloat16)  # noqa: E731
+    A, B, h = rand(2, r, K), rand(2, N, r), torch.randn(n, r, generator=gen, device="cuda")
+    off = torch.tensor([0, 130, n], device="cuda")
+    rows = torch.randperm(n, generator=gen, device="cuda")
+    far = torch.cat([torch.arange(4, device="cuda"), T - n + torch.arange(4, n, device="cuda")])[rows].to(torch.int32)
+    x, dy = rand(n, K), rand(n, N)
+    q = g.quantize_act8(x)
+    big_x, big_dy = torch.zeros(T, K, dtype=torch.bfloat16, device="cuda"), torch.zeros(T, N, dtype=torch.bfloat16, device="cuda")
+    big_x[far.long()], big_dy[far.long()] = x, dy
+    for dt in (torch.bfloat16, torch.float32):
+        want = g.lora_backward(dy, h, A, B, off, x=x, grad_dtype=dt)
+        got = g.lora_backward(big_dy, h, A, B, off, x=big_x, row_token=far, row_src=far, grad_dtype=dt)
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+    del big_x
+    codes, scales = torch.zeros(T, K, dtype=torch.int8, device="cuda"), torch.zeros(T, K // 32, dtype=torch.uint8, device="cuda")
+    codes[far.long()], scales[far.long()] = q
+    for rank in (r, 16):
+        a, b, hh = A[:, :rank].contiguous(), B[:, :, :rank].contiguous(), h[:, :rank].contiguous()
+        want = g.lora_backward(dy, hh, a, b, off, act8=q)
+        got = g.lora_backward(big_dy, hh, a, b, off, act8=(codes, scales), row_token=far, row_src=far)
+        assert all(torch.equal(u, v) for u, v in zip(got, want))
+
+
+def test_rows_far_into_h():
+    # more than 2^31 elements of h and grad_h; the last rows belong to an adapter of their own
+    g = lib()
+    r, R, last = 72, (1 << 25) - 700, 50
+    gen = torch.Generator(device="cuda").manual_seed(1)
+    rand = lambda *s: torch.randn(*s, generator=gen, device="cuda").to(torch.bfloat16)  # noqa: E731
+    A, B, x, dy = rand(2, r, 8), rand(2, 8, r), rand(R, 8), rand(R, 8)
+    off = torch.tensor([0, R - last, R], device="cuda")
+    h, gh = torch.empty(R, r, device="cuda"), torch.empty(R, r, device="cuda")
+    out = g.lora_apply(torch.zeros_like(dy), x, A, B, off, h=h)
+    dx, dA, dB = g.lora_backward(dy, h, A, B, off, x=x, grad_h=gh, grad_dtype=torch.float32)
+    tail = slice(R - last, R)
+    o = np.array([0, last])
+    want, wh, bound = LO.lora_apply_f64(np.zeros((last, 8)), f64(x[tail]), f64(A[1:]), f64(B[1:]), o)
+    near(h[tail], wh, np.abs(f64(x[tail])) @ np.abs(f64(A[1])).T, 8 + 32, 3, "h")
+    near(out[tail], want, bound, 8 + r + 32, 2, "out", np.zeros((last, 8)), r)
+    w = LO.lora_backward_f64(f64(dy[tail]), f64(x[tail]), f64(h[tail]), f64(A[1:]), f64(B[1:]), o)
+    near(gh[tail], w["grad_h"], w["grad_h_bound"], 8 + 32, 3, "grad_h")
+    near(dx[tail], w["dx"], w["dx_bound"], 8 + r + 32, 2, "dx", np.zeros((last, 8)), r)
+    near(dA[1:], w["dA"], w["dA_bound"], 8 + last + 32, 3, "dA")
+    near(dB[1:], w["dB"], w["dB_bound"], last + 32, 3, "dB")
+
+
+@pytest.mark.parametrize("r", [8, 40])
+@pytest.mark.parametrize("R", [3, 2400])
+def test_largest_axes(r, R):
+    # K or N at their limit; entries of -1, 0 and 1 whose sums fp32 holds exactly
+    g = lib()
+    big, gen = 1 << 24, torch.Generator(device="cuda").manual_seed(r)
+    few = lambda *s: torch.randint(-1, 2, s, generator=gen, device="cuda", dtype=torch.int8).to(torch.bfloat16)  # noqa: E731
+    off = torch.tensor([0, R], device="cuda")
+    tok = torch.arange(R, device="cuda", dtype=torch.int32) % 3
+    long_, short = few(3, big), few(3, 8)
+    # forward down the long axis, and the gradient of B along it
+    A, B = few(1, r, big), few(1, 8, r)
+    h = torch.empty(R, r, device="cuda")
+    out = g.lora_apply(torch.zeros(R, 8, device="cuda").bfloat16(), long_, A, B, off, row_token=tok, h=h)
+    want = sum(a.double() @ b.double().T for a, b in zip(long_.split(1 << 21, 1), A[0].split(1 << 21, 1)))
+    assert torch.equal(h.double(), want[tok.long()])
+    assert torch.equal(out, (want @ B[0].double().T)[tok.long()].to(torch.bfloat16))
+    ones = torch.ones(R, r, device="cuda")
+    dB = g.lora_backward(long_, ones, few(1, r, 8), few(1, big, r), off, x=short, row_token=tok, row_src=tok, want_dx=False)[2]
+    times = torch.bincount(tok.long(), minlength=3).double()
+    assert torch.equal(dB[0], (times @ long_.double())[:, None].expand(big, r).to(torch.bfloat16))
+    del dB
+    # out along the long axis
+    if R == 3:
+        A, B = few(1, r, 8), few(1, big, r)
+        want = (long_.double() + (short.double() @ A[0].double().T) @ B[0].double().T).to(torch.bfloat16)
+        assert torch.equal(g.lora_apply(long_, short, A, B, off, row_token=tok), want)
+
+
+def test_totals_beside_other_tensor_memory_kernels():
+    # gradient sums with totals in tensor memory, larger ranks and projections, on three streams and captured
+    g = lib()
+    Wd, Sd, _, _ = build_stack("nf4", 4, 256, 512)
+    x = torch.randn(4096, 512, device="cuda").to(torch.bfloat16)
+    off = torch.tensor([0, 1000, 1000, 3000, 4096], device="cuda")
+    want_y = g.grouped_gemm("nf4", x, Wd, Sd, off, R=4096)
+    calls = []
+    for r, counts in ((16, [9000, 5, 700] + [30] * 60), (32, [20000]), (64, [9000, 40]), (128, [5000, 5000])):
+        p = Problem(counts, r, 520, 776, seed=r)
+        dy, h = torch.randn_like(p.base), torch.randn(p.R, r, device="cuda")
+        calls.append(lambda p=p, dy=dy, h=h: g.lora_backward(dy, h, p.A, p.B, p.offsets, x=p.x, row_src=p.dest,
+                                                             grad_dtype=torch.float32, **p.rows()))
+    want = [call() for call in calls]
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        captured = [call() for call in calls]
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    for turn in range(3):
+        torch.cuda.synchronize()
+        with torch.cuda.stream(streams[0]):
+            ys = [g.grouped_gemm("nf4", x, Wd, Sd, off, R=4096) for _ in range(4)]
+        with torch.cuda.stream(streams[1]):
+            got = [call() for call in reversed(calls)][::-1]
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(y, want_y) for y in ys)
+        for outs in (got, captured):
+            assert all(torch.equal(u, v) for a, b in zip(outs, want) for u, v in zip(a, b))
+    g.device_status()
 
 
 def test_captured_calls_replay_and_share_nothing():
