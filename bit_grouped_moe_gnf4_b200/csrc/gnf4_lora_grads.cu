@@ -311,42 +311,7 @@ __device__ __forceinline__ void grad_body(const LoraGradArgs& p, const LoraGradS
         }
         __syncthreads();
     }
-    // the cluster's CTAs share the columns out and add up theirs, in place: no other CTA reads those
-    const int own = CW / parts, own0 = part * own;
-    if (parts > 1) {
-        cluster_arrive();
-        cluster_wait();
-        for (int i = tid; i < RP * own / 4; i += kLoraThreads) {
-            const int j = i / (own / 4), n = own0 + 4 * (i % (own / 4));
-            float* at = s_red + (size_t)(n / S::SC) * RP * S::kStride + j * S::kStride + n % S::SC;
-            *reinterpret_cast<float4*>(at) = cluster_sum(at, parts);
-        }
-        cluster_arrive();                                // a CTA's sums are read until here
-        __syncthreads();
-    }
-    // eight at a time along the gradient's contiguous axis: its columns (dA) or the rank (dB); C
-    // and r are multiples of 8
-    for (int i = tid; i < own * RP / 8; i += kLoraThreads) {
-        // dA: (rank, columns n..); dB: (column, ranks j..), the pieces of a column's ranks in turn
-        const int j = d.transposed ? 8 * (i % (RP / 8)) : i / (own / 8);
-        const int n = own0 + (d.transposed ? i / (RP / 8) : 8 * (i % (own / 8)));
-        if (j >= p.r || col0 + n >= d.C) continue;
-        const float* at = s_red + (size_t)(n / S::SC) * RP * S::kStride + j * S::kStride + n % S::SC;
-        const int next = d.transposed ? S::kStride : 1;
-        float v[8];
-#pragma unroll
-        for (int k = 0; k < 8; ++k) v[k] = at[k * next];
-        const int64_t o = (int64_t)e * p.r * d.C + (d.transposed ? (int64_t)(col0 + n) * p.r + j : (int64_t)j * d.C + col0 + n);
-        if constexpr (TERMS == 3) {
-            float4* to = reinterpret_cast<float4*>(reinterpret_cast<float*>(d.out) + o);
-            to[0] = make_float4(v[0], v[1], v[2], v[3]);
-            to[1] = make_float4(v[4], v[5], v[6], v[7]);
-        } else {
-            *reinterpret_cast<uint4*>(reinterpret_cast<uint16_t*>(d.out) + o) =
-                make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
-        }
-    }
-    if (parts > 1) cluster_wait();
+    store_sums<RP, CW, S::SC, S::kStride, TERMS>(p, d, it, s_red);
 }
 
 template <int RP, int WR, int TERMS, bool Q8, bool MANY>
