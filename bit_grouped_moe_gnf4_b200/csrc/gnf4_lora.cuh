@@ -13,8 +13,8 @@
 // ones keep the tensor pipe busy for 14 to 20 % of the time over many rows at ranks up to 32, and
 // longest at rank 64: 28 % over 4096 rows, 2880 -> 5760, 34 % in the backward's first half over 8192.
 //
-// Rounding: sums are fp32; a matrix instruction cuts its accumulator off at 24 bits, which the sums
-// over an adapter's rows make up for (gnf4_lora_grads.cuh). h (and g) enter the second product as two 16-bit terms, the value's
+// Rounding: sums are fp32; long ones are cut into chains of matrix instructions, whose sums are added
+// up rounded to nearest (kSumChain below, and kGradChain for the sums over rows). h (and g) enter the second product as two 16-bit terms, the value's
 // rounding and that of its remainder: about 17 significant bits, so that what the caller sees
 // is the one rounding of the output. For fp16 they are first scaled by a power of two per row,
 // so that neither term leaves the type's range. The gradient sums take two terms for bf16
@@ -35,6 +35,11 @@ namespace gnf4 {
 constexpr int kLoraThreads = 256;
 constexpr size_t kMaxSmem = 227 * 1024 - 512;      // dynamic shared memory of a CTA beside its static part
 constexpr int kLoraWarps = kLoraThreads / 32;
+// A matrix instruction cuts its accumulator off at 24 bits instead of rounding it (2^-25.8 of the sum on
+// average, always to the same side), so after so many steps (two instructions each) of the first product
+// a warp adds its accumulators to the partial sums and starts from nothing: up to 4096
+// columns there is one such chain, 2^-20.8 short.
+constexpr int kSumChain = 16;
 constexpr long long kStallWaitCycles = 1LL << 17;   // where a test wants a wait to give up
 
 __device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {

@@ -98,8 +98,8 @@ struct RowsShape {
 // BWD: the backward's chain (first factor [L, C, r], second [L, r, O]) instead of the forward's
 // ([L, r, C], [L, O, r]). A row that does not exist is computed from an address that does and
 // not stored (rows do not mix), so only the last piece of an axis that is no multiple of 32
-// is guarded element by element.
-template <int RP, bool BWD, bool F16>
+// is guarded element by element. LONG: a warp's part of the contraction is more than one chain.
+template <int RP, bool BWD, bool F16, bool LONG>
 __global__ void __launch_bounds__(kLoraThreads, RowsShape<RP>::kCtas) lora_rows_kernel(const LoraRowsArgs p) {
     using S = RowsShape<RP>;
     constexpr int BM = S::BM, NT = S::NT, KS = S::KS;
@@ -136,10 +136,6 @@ __global__ void __launch_bounds__(kLoraThreads, RowsShape<RP>::kCtas) lora_rows_
         const uint16_t* down = p.down + (int64_t)e * p.r * p.C +
                                (BWD ? (int64_t)(8 * (g >> 1) + (g & 1)) * p.r + 2 * V * t : (int64_t)g * p.C + 8 * t);
         float acc[NT][4];
-#pragma unroll
-        for (int c = 0; c < NT; ++c)
-#pragma unroll
-                for (int j = 0; j < 4; ++j) acc[c][j] = 0.0f;
         auto step = [&](int k0, auto guard) {
             constexpr bool GUARD = decltype(guard)::value;
             const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
@@ -186,32 +182,40 @@ __global__ void __launch_bounds__(kLoraThreads, RowsShape<RP>::kCtas) lora_rows_
         };
         const int whole = p.C / 32;
         const int st0 = (int)((int64_t)whole * part / parts), st1 = (int)((int64_t)whole * (part + 1) / parts);
-#pragma unroll 2
-        for (int st = st0; st < st1; ++st) step(32 * st, std::false_type{});
-        if (part == parts - 1 && (p.C & 31)) step(32 * whole, std::true_type{});
-        // partial sums: tile c, column index n of the MMA is rank 8c + n (forward), or
-        // 8 V (c / V) + 2 V (n >> 1) + 2 (c % V) + (n & 1) (backward). The upper four warps put
-        // theirs down, the lower four add their own on top.
         float* mine = s_red + (size_t)(warp & 3) * BM * S::kRed;
+        const int chains = LONG ? (whole / parts + kSumChain) / kSumChain : 1;  // of the warp with the most steps
+        for (int i = 0; i < chains; ++i) {
 #pragma unroll
-        for (int turn = 0; turn < 2; ++turn) {
-            if ((warp < 4) == (turn == 1)) {
+            for (int c = 0; c < NT; ++c)
 #pragma unroll
-                for (int h = 0; h < 2; ++h)
+                for (int j = 0; j < 4; ++j) acc[c][j] = 0.0f;
+            const int from = st0 + i * kSumChain, to = LONG ? min(from + kSumChain, st1) : st1;
+#pragma unroll 2
+            for (int st = from; st < to; ++st) step(32 * st, std::false_type{});
+            if (i == chains - 1 && part == parts - 1 && (p.C & 31)) step(32 * whole, std::true_type{});
+            // partial sums: tile c, column index n of the MMA is rank 8c + n (forward), or
+            // 8 V (c / V) + 2 V (n >> 1) + 2 (c % V) + (n & 1) (backward). The upper four warps put
+            // theirs down, the lower four add their own on top.
+#pragma unroll
+            for (int turn = 0; turn < 2; ++turn) {
+                if ((warp < 4) == (turn == 1)) {
+#pragma unroll
+                    for (int h = 0; h < 2; ++h)
 #pragma unroll
                         for (int c = 0; c < NT; ++c) {
                             const int j = BWD ? 8 * V * (c / V) + 2 * V * t + 2 * (c % V) : 8 * c + 2 * t;
                             float2* at = reinterpret_cast<float2*>(mine + (8 * h + g) * S::kRed + j);
                             float2 v = make_float2(acc[c][2 * h], acc[c][2 * h + 1]);
-                            if (turn == 1) {
+                            if (turn == 1 || i > 0) {
                                 const float2 o = *at;
                                 v.x += o.x;
                                 v.y += o.y;
                             }
                             *at = v;
                         }
+                }
+                __syncthreads();
             }
-            __syncthreads();
         }
     }
     if (CS > 1) {
@@ -412,7 +416,9 @@ cudaError_t launch_rows_t(const LoraRowsArgs& a, cudaStream_t s) {
     at[0].val.clusterDim.z = 1;
     cfg.attrs = at;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, lora_rows_kernel<RP, BWD, F16>, a);
+    // the loop over chains takes 0.2 of 5.8 us of a token at 2048 columns, which are one chain
+    if (a.C / 32 / (cs * kLoraWarps) < kSumChain) return cudaLaunchKernelEx(&cfg, lora_rows_kernel<RP, BWD, F16, false>, a);
+    return cudaLaunchKernelEx(&cfg, lora_rows_kernel<RP, BWD, F16, true>, a);
 }
 
 template <int RP>

@@ -284,42 +284,42 @@ __global__ void __launch_bounds__(StreamShape<RP, ROWS>::kThreads, 1) lora_strea
         float mine_fac = p.scaling ? __ldg(p.scaling + e) : 1.0f;
         if (p.weight && mine_row < rows) mine_fac *= __ldg(p.weight + row0 + mine_row);
 
-        float acc[MT][NT][4];
+        for (int q0 = 0; q0 < n1; q0 += kSumChain) {
+            float acc[MT][NT][4];
 #pragma unroll
-        for (int m = 0; m < MT; ++m)
+            for (int m = 0; m < MT; ++m)
 #pragma unroll
-            for (int c = 0; c < NT; ++c)
+                for (int c = 0; c < NT; ++c)
 #pragma unroll
-                for (int j = 0; j < 4; ++j) acc[m][c][j] = 0.0f;
-        for (int q = 0; q < n1; ++q) {
-            if (q) wait_stage();
-            const uint32_t at = (uint32_t)(slot * S::kStage), factor = ring + at + BM * S::kRow;
-            if (!gone) {                                             // columns past the end are zeros in both
+                    for (int j = 0; j < 4; ++j) acc[m][c][j] = 0.0f;
+            for (int q = q0; q < min(q0 + kSumChain, n1); ++q) {
+                if (q) wait_stage();
+                const uint32_t at = (uint32_t)(slot * S::kStage), factor = ring + at + BM * S::kRow;
+                if (!gone) {                                         // columns past the end are zeros in both
 #pragma unroll
-                for (int half = 0; half < 2; ++half) {
-                    uint32_t a[MT][4];
+                    for (int half = 0; half < 2; ++half) {
+                        uint32_t a[MT][4];
 #pragma unroll
-                    for (int m = 0; m < MT; ++m) ldmatrix4(a[m], rows_frag + at + 16 * m * S::kRow + 32 * half);
+                        for (int m = 0; m < MT; ++m) ldmatrix4(a[m], rows_frag + at + 16 * m * S::kRow + 32 * half);
 #pragma unroll
-                    for (int c = 0; c < NT; c += 2) {
-                        uint32_t b[4];                               // tile c: k 0-7, 8-15; tile c + 1: the same
-                        if constexpr (!BWD)
-                            ldmatrix4(b, factor + (8 * c + by_n) * S::kRow + 2 * k0 + 32 * half + 16 * by_k);
-                        else
-                            ldmatrix4_trans(b, factor + S::rank_at(k0 + 16 * half + (int)by_row, c + (lane >> 4)));
+                        for (int c = 0; c < NT; c += 2) {
+                            uint32_t b[4];                           // tile c: k 0-7, 8-15; tile c + 1: the same
+                            if constexpr (!BWD)
+                                ldmatrix4(b, factor + (8 * c + by_n) * S::kRow + 2 * k0 + 32 * half + 16 * by_k);
+                            else
+                                ldmatrix4_trans(b, factor + S::rank_at(k0 + 16 * half + (int)by_row, c + (lane >> 4)));
 #pragma unroll
-                        for (int m = 0; m < MT; ++m) {
-                            mma16<F16>(acc[m][c], a[m][0], a[m][1], a[m][2], a[m][3], b[0], b[1]);
-                            mma16<F16>(acc[m][c + 1], a[m][0], a[m][1], a[m][2], a[m][3], b[2], b[3]);
+                            for (int m = 0; m < MT; ++m) {
+                                mma16<F16>(acc[m][c], a[m][0], a[m][1], a[m][2], a[m][3], b[0], b[1]);
+                                mma16<F16>(acc[m][c + 1], a[m][0], a[m][1], a[m][2], a[m][3], b[2], b[3]);
+                            }
                         }
                     }
                 }
+                release_stage();
             }
-            release_stage();
-        }
-        // partial sums; with room for four only, the upper four warps put theirs down first and
-        // the lower four add their own on top
-        {
+            // partial sums; with room for four only, the upper four warps put theirs down first and
+            // the lower four add their own on top
             float* mine = s_red + (size_t)(warp & (S::kSums - 1)) * BM * S::kRed;
 #pragma unroll
             for (int turn = 0; turn < kLoraWarps / S::kSums; ++turn) {
@@ -332,7 +332,7 @@ __global__ void __launch_bounds__(StreamShape<RP, ROWS>::kThreads, 1) lora_strea
                             for (int c = 0; c < NT; ++c) {
                                 float2* o = reinterpret_cast<float2*>(mine + (16 * m + 8 * h + g) * S::kRed + 8 * c + 2 * t);
                                 float2 v = make_float2(acc[m][c][2 * h], acc[m][c][2 * h + 1]);
-                                if (turn == 1) {
+                                if (turn == 1 || q0 > 0) {
                                     const float2 u = *o;
                                     v.x += u.x;
                                     v.y += u.y;

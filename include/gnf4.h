@@ -437,9 +437,9 @@ gnf4_status gnf4_swiglu_backward(const void* grad_out, const void* gate_up, cons
  * Outputs may not overlap inputs, except that out may be base.
  * L in [1, 2048], r in [8, 128] with r % 8 == 0, K and N multiples of 8 up to 2^24, R at most
  * 2^30. 16-bit buffers and h are 16-byte aligned, row arrays and scaling 4-byte, offsets 8-byte.
- * Sums in fp32 by matrix instructions, which cut off what is below 24 bits: h (and grad_h) falls
- * short by about K 2^-33 (N 2^-33) of the sum of its products' magnitudes, 2^-20 at 8192. h enters
- * the second product with about 17 significant bits (two 16-bit terms).
+ * Sums in fp32: over any K (and N) h and grad_h are off by no more than about 2^-20 of the sum of
+ * their products' magnitudes. h enters the second product with about 17 significant bits (two
+ * 16-bit terms).
  * Deterministic: the same call gives the same bits. A row's bits (out and h, the backward's dx and
  * grad_h) do not depend on the other rows as long as R and L are the same, whatever the offsets
  * say: a captured call gives a token the same bits in every batch. Calls of another R or L may
@@ -476,8 +476,8 @@ gnf4_status gnf4_lora_apply(const void* base, const void* x, int dtype, const vo
  *            are saved, the product behind it is computed all the same)
  * grad_h     device fp32 [R, r] (written)
  * dA, dB     device [L, r, K] and [L, N, r] of grad_dtype: GNF4_DTYPE_BF16 or GNF4_DTYPE_F32
- *            (fp32 sums, rounded once; over any number of rows fp32 results fall short by no
- *            more than about 2^-20 of the sum of magnitudes). dA may be NULL, and then x is not given either: a
+ *            (fp32 sums, rounded once; over any number of rows fp32 results are off by no more
+ *            than about 2^-20 of the sum of magnitudes). dA may be NULL, and then x is not given either: a
  *            layer that has x back only later takes it from gnf4_lora_grad_a
  * Outputs may not overlap inputs or one another, except that dx may be dx_base.
  * Other arguments, limits and errors as in gnf4_lora_apply. Rows at or behind
