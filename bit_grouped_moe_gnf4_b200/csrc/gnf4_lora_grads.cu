@@ -5,7 +5,8 @@
 // stages of 32 WR: the rows of `right` are gathered into shared memory by 16-byte asynchronous
 // copies, three stages deep (the gather's latency, index then row, is what a warp alone cannot
 // hide), while `left` is read ahead by a stage into registers and split into its 16-bit terms
-// once for all warps. Both fragments come out of shared memory transposed.
+// once for all warps. Both fragments come out of shared memory transposed. Over many rows the
+// accumulators are emptied into totals in tensor memory from time to time (kGradChain).
 //
 // What bounds it is instruction issue: about 330 instructions a warp and stage of 32 rows (the
 // copies' addresses, the split of left, the products; 450 with codes). 128 experts over 32768 rows,
